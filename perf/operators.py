@@ -44,9 +44,9 @@ def listed():
         # one token through a whole 8B layer, the step that a decode loop repeats for every layer
         dict(name="decode layer 8B", kind="decode", T=1, r=16, adapter=True, h=h, kv=kv, m=m),
         # eight sequences at once through the largest projection (72B down)
-        dict(name="decode down 72B, 8 tokens", kind="decode", T=8, r=16, adapter=True, K=29568, N=8192),
+        dict(name="decode down 72B 8 tokens", kind="decode", T=8, r=16, adapter=True, K=29568, N=8192),
         # an odd number of tokens with the adapter off: the reference model's answers, 0.5B shapes
-        dict(name="decode layer 0.5B, 13 tokens", kind="decode", T=13, r=16, adapter=False, h=896, kv=128, m=4864),
+        dict(name="decode layer 0.5B 13 tokens", kind="decode", T=13, r=16, adapter=False, h=896, kv=128, m=4864),
         # a short pair scored by the reference model over the whole vocabulary: few rows, long ones
         dict(name="score 1 pair", kind="score", T=37, P=1, V=VOCAB, pad=0, dtype="bf16", prompt=0.3, tail=0, average=False),
         # the reference pass over a full batch
