@@ -284,6 +284,44 @@ lsn_status lora_layer_fwd(int n, const lsn_lora_proj* p, int64_t T, int r, float
 lsn_status lora_layer_bwd(int n, const lsn_lora_proj* p, int64_t T, int r, float scale, int accumulate,
                           void* ws, size_t ws_bytes, lsn_stream_t stream);
 
+/* ------------------------------------------------- a handful of tokens ---
+ *
+ * The same linears for a model that answers: T <= LSN_DECODE_MAX_T tokens (one
+ * per sequence being generated, or a few drafted ones) through frozen NF4
+ * bases and their adapters,
+ *
+ *   y[t, n] = sum over blocks b of a[n, b] * (sum over k in b of level[code[n, k]] * x[t, k])
+ *             + s sum_j (x A^T)[t, j] B[n, j],
+ *
+ * read straight from the packed codes: at this size the time is that of
+ * reading the weights, and a bf16 copy of W would be nine times the bytes.
+ * Precision: the weights enter as level (fp16, 11 significant bits) times the
+ * fp32 absmax and are not rounded to bf16 as lora_linear_fwd's are, x enters
+ * exactly (fp16 times a power of two per block), all sums are fp32, x A^T
+ * stays fp32, and y is rounded once.  y therefore agrees with
+ * lora_linear_fwd's to the rounding of its weights, not bit for bit; the
+ * sum's order depends on the shapes alone.
+ *
+ * Shapes as lora_layer_fwd (K % 64 == 0, N % 64 == 0, r a multiple of 8 up to
+ * 64), 0 <= T <= LSN_DECODE_MAX_T (T == 0 is a no-op); NF4 bases only
+ * (LSN_ERR_UNSUPPORTED for a bf16 base).  A and B both NULL: the adapter is
+ * off.  Of a descriptor, W, x, A, B and y are used; group has no effect.
+ * Projections with the same x pointer and K share its preparation.  y may
+ * overlap no input and no other y. */
+#define LSN_DECODE_MAX_T 16
+
+/* Workspace bytes of lora_linear_decode (n = 1) and lora_layer_decode for these
+ * projections, at most T tokens and this rank (0 when an argument is invalid).
+ * It need not be zeroed. */
+size_t lsn_decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r);
+
+lsn_status lora_linear_decode(const lsn_base* W, const uint16_t* x, int64_t T, const uint16_t* A, const uint16_t* B,
+                              int r, float scale, uint16_t* y, void* ws, size_t ws_bytes, lsn_stream_t stream);
+
+/* All projections of a layer (n <= LSN_LAYER_MAX_PROJ) in the same two launches. */
+lsn_status lora_layer_decode(int n, const lsn_lora_proj* p, int64_t T, int r, float scale, void* ws, size_t ws_bytes,
+                             lsn_stream_t stream);
+
 /* Synchronise `stream`, then read the status word at the start of a LoRA
  * workspace: LSN_ERR_TIMEOUT if a tensor-core kernel gave up on a bounded
  * wait since the last check (the word is then cleared), LSN_OK otherwise.
@@ -312,7 +350,8 @@ typedef enum {
     LSN_K_LORA_DOWN = 3,  /* u = x A^T, g = dY B                 (bytes) */
     LSN_K_LORA_TGRAD = 4, /* dA, dB token reductions             (bytes) */
     LSN_K_QUANTIZE = 5,   /* fp32 -> NF4                         (bytes) */
-    LSN_K_COUNT = 6
+    LSN_K_DECODE = 6,     /* few-token NF4 linears               (bytes) */
+    LSN_K_COUNT = 7
 } lsn_kernel_kind;
 
 typedef struct {

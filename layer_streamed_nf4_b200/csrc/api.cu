@@ -441,13 +441,40 @@ lsn_status timed_gemm(int kind, const uint16_t* A, int64_t lda, const uint16_t* 
     return launch_gemm(A, lda, B, ldb, b_mn, LA, LB, r, M, N, Kc, D, ldd, err, st, split);
 }
 
+lsn_status decode_call(int n, const lsn_lora_proj* p, int64_t T, int r, float scale, void* ws, size_t ws_bytes,
+                       lsn_stream_t stream, const char* who) {
+    const std::string f(who);
+    LSN_CHECK_ARG(n >= 1 && n <= LSN_LAYER_MAX_PROJ, f + ": n must be in [1, LSN_LAYER_MAX_PROJ]");
+    LSN_CHECK_ARG(p != nullptr, f + ": projection array is NULL");
+    LSN_CHECK_ARG(T >= 0 && T <= LSN_DECODE_MAX_T, f + ": T must be in [0, LSN_DECODE_MAX_T]");
+    double bytes = 0.0;
+    for (int i = 0; i < n; ++i) {
+        const std::string fi = n > 1 ? f + ": projection " + std::to_string(i) : f;
+        lsn_status s = check_proj(&p[i].W, p[i].x, T, p[i].A, p[i].B, r, fi, true);
+        if (s != LSN_OK) return s;
+        if (p[i].W.kind != LSN_BASE_NF4) return fail(LSN_ERR_UNSUPPORTED, fi + ": the few-token linears take NF4 bases");
+        LSN_CHECK_ARG((p[i].y != nullptr || T == 0) && aligned16(p[i].y), fi + ": y must be a 16-byte aligned device pointer");
+        const double N = (double)p[i].W.rows, K = (double)p[i].W.cols;
+        bytes += N * K / 2.0 + N * K / 64.0 + N * K / 4096.0 + 2.0 * T * (K + N) + (adapter_off(p[i]) ? 0.0 : 2.0 * r * (K + N));
+    }
+    if (T == 0) return LSN_OK;
+    LSN_CHECK_ARG(ws != nullptr && aligned16(ws), f + ": workspace must be a 16-byte aligned device pointer");
+    const size_t need = decode_ws_bytes(n, p, T, r);
+    LSN_CHECK_ARG(ws_bytes >= need, f + ": workspace too small (need " + std::to_string(need) + " bytes)");
+    lsn_status s = check_device();
+    if (s != LSN_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    TimingScope ts(LSN_K_DECODE, bytes, st, 2);
+    return launch_decode(n, p, (int)T, r, scale, ws, st);
+}
+
 }  // namespace
 
 extern "C" {
 
 const char* lsn_last_error(void) { return g_last_error.c_str(); }
 
-int lsn_version(void) { return 100; }
+int lsn_version(void) { return 200; }
 
 void lsn_nf4_codebook(float out[16]) { std::memcpy(out, nf4_tables().level, sizeof(float) * 16); }
 
@@ -993,6 +1020,32 @@ lsn_status lora_layer_bwd(int n, const lsn_lora_proj* p, int64_t T, int r, float
         }
     }
     return lanes.join();
+}
+
+size_t lsn_decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r) {
+    if (n < 1 || n > LSN_LAYER_MAX_PROJ || p == nullptr || T < 0 || T > LSN_DECODE_MAX_T || r < 8 || r > 64 || r % 8) return 0;
+    for (int i = 0; i < n; ++i)
+        if (p[i].W.rows <= 0 || p[i].W.cols <= 0 || p[i].W.cols > (int64_t)1 << 30) return 0;
+    return decode_ws_bytes(n, p, T, r);
+}
+
+lsn_status lora_layer_decode(int n, const lsn_lora_proj* p, int64_t T, int r, float scale, void* ws, size_t ws_bytes,
+                             lsn_stream_t stream) {
+    NvtxRange nvtx("lora_layer_decode");
+    return decode_call(n, p, T, r, scale, ws, ws_bytes, stream, "lora_layer_decode");
+}
+
+lsn_status lora_linear_decode(const lsn_base* W, const uint16_t* x, int64_t T, const uint16_t* A, const uint16_t* B,
+                              int r, float scale, uint16_t* y, void* ws, size_t ws_bytes, lsn_stream_t stream) {
+    NvtxRange nvtx("lora_linear_decode");
+    LSN_CHECK_ARG(W != nullptr, "lora_linear_decode: base is NULL");
+    lsn_lora_proj p{};
+    p.W = *W;
+    p.x = x;
+    p.A = A;
+    p.B = B;
+    p.y = y;
+    return decode_call(1, &p, T, r, scale, ws, ws_bytes, stream, "lora_linear_decode");
 }
 
 lsn_status lsn_set_option(int option, int value) {

@@ -51,6 +51,7 @@ EXPORTS = (
     "nf4_quantize_noalloc", "lsn_set_option", "lsn_get_option", "lsn_gemm_merged_schedule",
     "lsn_layer_ws_bytes", "lora_layer_fwd", "lora_layer_bwd", "nf4_dequant_batch",
     "lsn_selftest_wait_timeout", "layer_pool_set_debug",
+    "lsn_decode_ws_bytes", "lora_linear_decode", "lora_layer_decode",
 )
 
 
@@ -79,12 +80,13 @@ class LoraProj(ctypes.Structure):
 
 LSN_LAYER_MAX_PROJ = 16
 
-KERNEL_KINDS = ("gemm_fwd", "gemm_bwd", "dequant", "lora_down", "lora_tgrad", "quantize")
+KERNEL_KINDS = ("gemm_fwd", "gemm_bwd", "dequant", "lora_down", "lora_tgrad", "quantize", "decode")
+_NK = len(KERNEL_KINDS)
 
 
 class KernelTiming(ctypes.Structure):
-    _fields_ = [("launches", ctypes.c_uint64 * 6), ("kernels", ctypes.c_uint64 * 6), ("ms", ctypes.c_double * 6),
-                ("work", ctypes.c_double * 6)]
+    _fields_ = [("launches", ctypes.c_uint64 * _NK), ("kernels", ctypes.c_uint64 * _NK), ("ms", ctypes.c_double * _NK),
+                ("work", ctypes.c_double * _NK)]
 
 
 class PoolStats(ctypes.Structure):
@@ -123,6 +125,9 @@ _sig("lsn_selftest_wait_timeout", _i, [_i, _vp])
 _sig("lsn_layer_ws_bytes", _sz, [_i, ctypes.POINTER(LoraProj), _i64, _i])
 _sig("lora_layer_fwd", _i, [_i, ctypes.POINTER(LoraProj), _i64, _i, ctypes.c_float, _vp, _sz, _vp])
 _sig("lora_layer_bwd", _i, [_i, ctypes.POINTER(LoraProj), _i64, _i, ctypes.c_float, _i, _vp, _sz, _vp])
+_sig("lsn_decode_ws_bytes", _sz, [_i, ctypes.POINTER(LoraProj), _i64, _i])
+_sig("lora_linear_decode", _i, [ctypes.POINTER(Base), _vp, _i64, _vp, _vp, _i, ctypes.c_float, _vp, _vp, _sz, _vp])
+_sig("lora_layer_decode", _i, [_i, ctypes.POINTER(LoraProj), _i64, _i, ctypes.c_float, _vp, _sz, _vp])
 _sig("lsn_set_option", _i, [_i, _i])
 _sig("lsn_get_option", _i, [_i])
 _IP = ctypes.POINTER(ctypes.c_int)
@@ -290,6 +295,29 @@ def lora_layer_bwd(projs, T: int, r: int, scale: float, accumulate: bool, ws, ws
     arr = projs if isinstance(projs, ctypes.Array) else proj_array(projs)
     _check(_lib.lora_layer_bwd(len(arr), arr, T, r, scale, int(bool(accumulate)), _ptr(ws), ws_bytes,
                                _stream(stream)), "lora_layer_bwd")
+
+
+# ---------------------------------------------------- a handful of tokens ---
+
+LSN_DECODE_MAX_T = 16
+
+
+def decode_ws_bytes(projs, T: int, r: int) -> int:
+    arr = projs if isinstance(projs, ctypes.Array) else proj_array(projs)
+    return _lib.lsn_decode_ws_bytes(len(arr), arr, T, r)
+
+
+def lora_linear_decode(W: Base, x, T: int, A, B, r: int, scale: float, y, ws, ws_bytes: int, stream=None):
+    """y = x W^T + scale (x A^T) B^T for T <= LSN_DECODE_MAX_T tokens, W an NF4 base read from its codes (A and B
+    None: adapter off)."""
+    _check(_lib.lora_linear_decode(ctypes.byref(W), _ptr(x), T, _ptr(A), _ptr(B), r, scale, _ptr(y), _ptr(ws),
+                                   ws_bytes, _stream(stream)), "lora_linear_decode")
+
+
+def lora_layer_decode(projs, T: int, r: int, scale: float, ws, ws_bytes: int, stream=None):
+    arr = projs if isinstance(projs, ctypes.Array) else proj_array(projs)
+    _check(_lib.lora_layer_decode(len(arr), arr, T, r, scale, _ptr(ws), ws_bytes, _stream(stream)),
+           "lora_layer_decode")
 
 
 def selftest_wait_timeout(limit_us: int = 1000, stream=None) -> int:
