@@ -335,6 +335,119 @@ lsn_status lsn_ws_status(void* ws, lsn_stream_t stream);
  * the context stays usable), LSN_ERR_STATE if it did not. */
 lsn_status lsn_selftest_wait_timeout(int limit_us, lsn_stream_t stream);
 
+/* ------------------------------------------------------ preference loss --
+ *
+ * Preference training ("An 8B Fine-Tune Now Fits in 4 GB of VRAM": the
+ * streamed base with the adapters switched off is the reference) compares two
+ * answers to a prompt through the log-probabilities that the model being
+ * trained and the reference model give them.  With logits l [T, V] of a packed
+ * batch, targets y [T] (the token that row t is to predict) and sequences i
+ * covering rows seq_start[i] .. seq_start[i+1):
+ *
+ *   lse_t  = log sum_v exp l[t, v]
+ *   logp_i = sum of (l[t, y_t] - lse_t) over the scored rows t of sequence i,
+ *            or their mean (average != 0; 0 when no row is scored)
+ *
+ * A row is scored when it lies in a sequence and 0 <= y_t < V; any other target
+ * (-100, say) marks a prompt or padding row, which is not read.  Sequences 2p
+ * and 2p+1 are pair p's chosen and rejected answer:
+ *
+ *   a = logp_2p - ref_2p,  b = logp_2p+1 - ref_2p+1,  h = a - b  (ref = 0 without a reference)
+ *   SIGMOID  (1-e) softplus(-beta h) + e softplus(beta h)        e = label_smoothing
+ *   HINGE    max(0, 1 - beta h)
+ *   SQUARED  (h - 1 / (2 beta))^2
+ *   mean_loss = mean over the pairs;  dlogp = grad_scale d mean_loss / d logp
+ *   dl[t, v]  = c_t ([v = y_t] - exp(l[t, v] - lse_t)),  c_t = dlogp of t's sequence
+ *               (/ its scored rows when average != 0), 0 in rows that are not scored
+ *
+ * Types: logits bf16 or fp32 with row stride ld >= V elements (rows need only
+ * their type's alignment; 16-byte aligned rows are read and written fastest),
+ * dlogits of the same type, in place (dlogits == logits, same stride) or
+ * apart.  Sums of exponentials fp32, sums over tokens and the loss fp64; logp
+ * is fp64, since the log ratios are small differences of large sums.
+ * seq_start is a DEVICE array of n_seq + 1 non-decreasing row numbers; every
+ * row 0..T-1 of dlogits and lse is written (zeros where not scored), columns
+ * V.. of a padded row are not touched.  seq_start may change between replays
+ * of a captured call.  Infinite logits: -infinity is a token that cannot
+ * occur; a row holding +infinity or NaN, or nothing but -infinity, makes its
+ * pair's loss and gradients NaN and no other's. */
+typedef enum { LSN_DT_BF16 = 0, LSN_DT_F32 = 1 } lsn_dtype;
+typedef enum { LSN_PREF_SIGMOID = 0, LSN_PREF_HINGE = 1, LSN_PREF_SQUARED = 2 } lsn_preference_kind;
+
+typedef struct {
+    const void* logits;        /* [T, V], row stride ld */
+    int64_t T, V, ld;
+    int dtype;                 /* lsn_dtype of logits and dlogits */
+    const int32_t* targets;    /* [T] */
+    int n_seq;
+    const int32_t* seq_start;  /* [n_seq + 1] */
+    int average;               /* logp_i: 0 the sum over the scored rows, 1 their mean */
+} lsn_seq_logits;
+
+typedef struct {
+    int kind;                  /* lsn_preference_kind */
+    float beta;                /* > 0 */
+    float label_smoothing;     /* [0, 0.5], SIGMOID only */
+    float grad_scale;          /* factor on the gradients alone (1 / accumulation steps, say) */
+} lsn_preference;
+
+/* Workspace bytes of seq_logp_fwd and preference_loss_* for these logits (T and
+ * V are looked at; 0 when they are invalid).  Zero-fill it once when it is
+ * allocated; calls that may run at the same time need one each. */
+size_t lsn_seq_logp_ws_bytes(const lsn_seq_logits* in);
+
+/* lse [T] fp32, logp [n_seq] fp64, count [n_seq] scored rows (may be NULL). */
+lsn_status seq_logp_fwd(const lsn_seq_logits* in, float* lse, double* logp, int32_t* count, void* ws, size_t ws_bytes,
+                        lsn_stream_t stream);
+
+/* dlogits from the gradient dlogp [n_seq] of any function of logp; lse and
+ * (average != 0) count as seq_logp_fwd wrote them for the same logits. */
+lsn_status seq_logp_bwd(const lsn_seq_logits* in, const float* lse, const float* dlogp, const int32_t* count,
+                        void* dlogits, int64_t ld_d, lsn_stream_t stream);
+
+/* seq_logp_fwd and the loss of n_seq / 2 pairs: ref_logp [n_seq] fp64 (what
+ * seq_logp_fwd gave for the reference's logits) or NULL, reward [n_seq] =
+ * beta (logp - ref) (may be NULL), loss [n_seq / 2], mean_loss [1] (may be
+ * NULL), dlogp [n_seq] for seq_logp_bwd. */
+lsn_status preference_loss_fwd(const lsn_seq_logits* in, const double* ref_logp, const lsn_preference* p, float* lse,
+                               double* logp, int32_t* count, float* reward, float* loss, float* mean_loss,
+                               float* dlogp, void* ws, size_t ws_bytes, lsn_stream_t stream);
+
+/* preference_loss_fwd and seq_logp_bwd in one call, for a training step. */
+lsn_status preference_loss_fwd_bwd(const lsn_seq_logits* in, const double* ref_logp, const lsn_preference* p,
+                                   float* lse, double* logp, int32_t* count, float* reward, float* loss,
+                                   float* mean_loss, float* dlogp, void* dlogits, int64_t ld_d, void* ws,
+                                   size_t ws_bytes, lsn_stream_t stream);
+
+/* -------------------------------------------- gradient norm and clipping --
+ *
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   dst  = g * min(1, max_norm / norm)
+ *
+ * over n tensors of any sizes (the dA and dB of a stack), fp32 or bf16 each.
+ * The sum is held in fp64 (squares of values too large or small for fp32
+ * included); its order depends on the sizes and alignments alone.  A norm that
+ * is infinite or NaN leaves the values unscaled and is reported as it is.
+ * t is a HOST array, read during the call only; its pointers need only their
+ * type's alignment, dst may equal src (in place; nothing is written when
+ * nothing is scaled) or lie apart, and the tensors may not overlap each other. */
+typedef struct {
+    const void* src;
+    void* dst;                 /* unused by grad_norm */
+    int64_t numel;
+    int dtype;                 /* lsn_dtype */
+} lsn_grad;
+
+/* Workspace bytes for n tensors.  Zero-fill it once when it is allocated. */
+size_t lsn_grad_ws_bytes(int n);
+
+/* norm [1] fp32 (device). */
+lsn_status grad_norm(int n, const lsn_grad* t, float* norm, void* ws, size_t ws_bytes, lsn_stream_t stream);
+
+/* norm as grad_norm (before clipping), and the clipped gradients; max_norm > 0. */
+lsn_status grad_clip(int n, const lsn_grad* t, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                     lsn_stream_t stream);
+
 /* ------------------------------------------------------- kernel timing --
  *
  * Optional per-launch timing of the library's own kernels: while enabled,
@@ -351,7 +464,10 @@ typedef enum {
     LSN_K_LORA_TGRAD = 4, /* dA, dB token reductions             (bytes) */
     LSN_K_QUANTIZE = 5,   /* fp32 -> NF4                         (bytes) */
     LSN_K_DECODE = 6,     /* few-token NF4 linears               (bytes) */
-    LSN_K_COUNT = 7
+    LSN_K_SEQ_LOGP = 7,   /* log-probabilities, preference loss  (bytes) */
+    LSN_K_SEQ_GRAD = 8,   /* gradient of the logits              (bytes) */
+    LSN_K_GRAD = 9,       /* gradient norm and clipping          (bytes) */
+    LSN_K_COUNT = 10
 } lsn_kernel_kind;
 
 typedef struct {

@@ -1,0 +1,290 @@
+// The global norm of many gradient tensors and their clipping:
+//   norm = sqrt(sum over tensors and elements of g^2),   dst = g min(1, max_norm / norm).
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "launch.cuh"
+#include "timing.cuh"
+
+namespace lsn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTensors = 1024;          // of one launch (28 bytes of kernel parameters each)
+constexpr int kChunkBytes = 16384;         // one CTA's piece of a tensor at a time
+constexpr int kMaxCtas = 2048;             // partial sums per launch
+
+// Tensors of one launch; tensor i covers chunks chunk0[i] .. chunk0[i + 1].
+struct GradArgs {
+    const void* src[kMaxTensors];
+    void* dst[kMaxTensors];
+    uint64_t numel[kMaxTensors];           // bit 63: bf16
+    int chunk0[kMaxTensors];
+    int n, chunks;
+};
+static_assert(sizeof(GradArgs) + 64 <= 32764, "kernel parameters");
+
+// Head of the workspace: the scale for the clip kernel, the count of finished
+// CTAs (zero between calls), then one fp64 partial sum per CTA and launch.
+struct GradWs {
+    float factor;
+    int done;
+    double part[1];
+};
+constexpr size_t kWsHead = 256;
+
+__device__ __forceinline__ int tensor_of(const GradArgs& a, int chunk) {
+    int lo = 0, hi = a.n - 1;              // the last tensor whose first chunk is <= chunk
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (a.chunk0[m] <= chunk) lo = m; else hi = m - 1;
+    }
+    return lo;
+}
+
+// A chunk is 16-byte words of src's own alignment: element e of the tensor is
+// element e + mis of the words that start at src - mis.
+struct Chunk {
+    const char* base;      // 16-byte aligned start of the chunk
+    int lo, hi;            // its elements' bounds within the tensor, in elements from base
+    bool bf16;
+};
+__device__ __forceinline__ Chunk chunk_of(const GradArgs& a, int i, int chunk) {
+    const uint64_t nm = a.numel[i];
+    Chunk c;
+    c.bf16 = nm >> 63;
+    const int es = c.bf16 ? 2 : 4;
+    const int64_t numel = (int64_t)(nm & ~(1ull << 63));
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.src[i]);
+    const int mis = (int)(p & 15) / es;
+    const int64_t at = (int64_t)(chunk - a.chunk0[i]) * (kChunkBytes / es);
+    c.base = reinterpret_cast<const char*>(p - (p & 15)) + at * es;
+    c.lo = at == 0 ? mis : 0;
+    const int64_t left = numel + mis - at;
+    c.hi = (int)(left < kChunkBytes / es ? left : kChunkBytes / es);
+    return c;
+}
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Sum of squares of up to 8 values: fp32 within a 16-byte word, fp64 above,
+// and in fp64 from the start where a square would leave fp32's normal range.
+__device__ __forceinline__ double squares4(float a, float b, float c, float d) {
+    const float s = fmaf(a, a, fmaf(b, b, fmaf(c, c, d * d)));
+    if (s < 3e38f && s > 1e-30f) return (double)s;
+    return (double)a * a + (double)b * b + (double)c * c + (double)d * d;
+}
+
+__device__ double block_sum(double v, double* sh) {
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = threadIdx.x < kThreads / 32 ? sh[threadIdx.x] : 0.0;
+    if (threadIdx.x < 32) {
+        #pragma unroll
+        for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;               // the sum, in thread 0
+}
+
+// Partial sums of one launch's tensors; with `last`, the last CTA to finish
+// adds those of every launch (`parts` in all, in order) and writes the norm.
+__global__ void __launch_bounds__(kThreads) lsn_grad_norm_kernel(const __grid_constant__ GradArgs a, GradWs* ws, int part0, int parts, bool last,
+                                                                 float max_norm, float* norm) {
+    __shared__ double sh[kThreads / 32];
+    __shared__ int is_last;
+    pdl_wait();
+    double sum = 0.0;
+    for (int ch = blockIdx.x; ch < a.chunks; ch += gridDim.x) {
+        const Chunk c = chunk_of(a, tensor_of(a, ch), ch);
+        const int per = c.bf16 ? 8 : 4;
+        for (int w = threadIdx.x; w * per < c.hi; w += kThreads) {
+            const int e = w * per;
+            if (e >= c.lo && e + per <= c.hi) {
+                const uint4 v = *reinterpret_cast<const uint4*>(c.base + 16 * w);
+                if (c.bf16)
+                    sum += squares4(lo_bf16(v.x), hi_bf16(v.x), lo_bf16(v.y), hi_bf16(v.y)) +
+                           squares4(lo_bf16(v.z), hi_bf16(v.z), lo_bf16(v.w), hi_bf16(v.w));
+                else
+                    sum += squares4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+            } else {
+                for (int k = max(e, c.lo); k < min(e + per, c.hi); ++k) {
+                    const double g = c.bf16 ? (double)lo_bf16(reinterpret_cast<const uint16_t*>(c.base)[k])
+                                            : (double)reinterpret_cast<const float*>(c.base)[k];
+                    sum += g * g;
+                }
+            }
+        }
+    }
+    sum = block_sum(sum, sh);
+    if (threadIdx.x == 0) {
+        ws->part[part0 + blockIdx.x] = sum;
+        is_last = 0;
+        if (last) {
+            __threadfence();
+            is_last = atomicAdd(&ws->done, 1) == (int)gridDim.x - 1;
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    if (!is_last) return;
+    double t = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kThreads) t += __ldcg(&ws->part[i]);
+    t = block_sum(t, sh);
+    if (threadIdx.x == 0) {
+        const double nrm = sqrt(t);
+        *norm = (float)nrm;
+        // over the largest norm: scale; a norm that is no number, or infinite, leaves the gradients as they are
+        ws->factor = nrm > (double)max_norm && nrm <= 1.7976931348623157e308 ? (float)((double)max_norm / nrm) : 1.f;
+        ws->done = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_constant__ GradArgs a, const GradWs* ws) {
+    pdl_wait();
+    const float f = ws->factor;
+    for (int ch = blockIdx.x; ch < a.chunks; ch += gridDim.x) {
+        const int i = tensor_of(a, ch);
+        const Chunk c = chunk_of(a, i, ch);
+        char* const dst = reinterpret_cast<char*>(a.dst[i]) + (c.base - reinterpret_cast<const char*>(a.src[i]));
+        if (f == 1.f && dst == c.base) continue;
+        const int es = c.bf16 ? 2 : 4;
+        const int per = 16 / es;
+        const bool wide = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+        for (int w = threadIdx.x; w * per < c.hi; w += kThreads) {
+            const int e = w * per;
+            if (wide && e >= c.lo && e + per <= c.hi) {
+                uint4 v = *reinterpret_cast<const uint4*>(c.base + 16 * w);
+                if (c.bf16) {
+                    v.x = pack_bf16x2(lo_bf16(v.x) * f, hi_bf16(v.x) * f);
+                    v.y = pack_bf16x2(lo_bf16(v.y) * f, hi_bf16(v.y) * f);
+                    v.z = pack_bf16x2(lo_bf16(v.z) * f, hi_bf16(v.z) * f);
+                    v.w = pack_bf16x2(lo_bf16(v.w) * f, hi_bf16(v.w) * f);
+                } else {
+                    v.x = __float_as_uint(__uint_as_float(v.x) * f);
+                    v.y = __float_as_uint(__uint_as_float(v.y) * f);
+                    v.z = __float_as_uint(__uint_as_float(v.z) * f);
+                    v.w = __float_as_uint(__uint_as_float(v.w) * f);
+                }
+                *reinterpret_cast<uint4*>(dst + 16 * w) = v;
+            } else {
+                for (int k = max(e, c.lo); k < min(e + per, c.hi); ++k) {
+                    if (c.bf16)
+                        reinterpret_cast<uint16_t*>(dst)[k] =
+                            __bfloat16_as_ushort(__float2bfloat16_rn(lo_bf16(reinterpret_cast<const uint16_t*>(c.base)[k]) * f));
+                    else
+                        reinterpret_cast<float*>(dst)[k] = reinterpret_cast<const float*>(c.base)[k] * f;
+                }
+            }
+        }
+    }
+}
+
+int64_t chunks_of(const lsn_grad& t) {
+    const int es = t.dtype == LSN_DT_BF16 ? 2 : 4;
+    const int64_t mis = (int64_t)(reinterpret_cast<uintptr_t>(t.src) & 15) / es;
+    return t.numel == 0 ? 0 : ceil_div(t.numel + mis, kChunkBytes / es);
+}
+
+template <class... P, class... A>
+lsn_status launch(void (*kernel)(P...), int grid, cudaStream_t st, A&&... args) {
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl_attr(at);
+    LSN_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return LSN_OK;
+}
+
+size_t ws_bytes_of(int n) { return kWsHead + 8 * (size_t)kMaxCtas * (size_t)std::max<int64_t>(1, ceil_div(n, kMaxTensors)); }
+
+lsn_status grad_call(int n, const lsn_grad* t, bool clip, float max_norm, float* norm, void* ws, size_t ws_bytes, lsn_stream_t stream,
+                     const char* who) {
+    const std::string f(who);
+    LSN_CHECK_ARG(n >= 0, f + ": n must be >= 0");
+    LSN_CHECK_ARG(n == 0 || t != nullptr, f + ": tensor array is NULL");
+    LSN_CHECK_ARG(!clip || (max_norm > 0.f && std::isfinite(max_norm)), f + ": max_norm must be positive and finite");
+    LSN_CHECK_ARG(norm != nullptr && (reinterpret_cast<uintptr_t>(norm) & 3) == 0, f + ": norm must be a 4-byte aligned device pointer");
+    LSN_CHECK_ARG(ws != nullptr && aligned16(ws), f + ": workspace must be a 16-byte aligned device pointer");
+    LSN_CHECK_ARG(ws_bytes >= ws_bytes_of(n), f + ": workspace too small (need " + std::to_string(ws_bytes_of(n)) + " bytes)");
+    int64_t chunks = 0;
+    double bytes = 0.0;
+    for (int i = 0; i < n; ++i) {
+        const std::string fi = f + ": tensor " + std::to_string(i);
+        LSN_CHECK_ARG(t[i].numel >= 0 && t[i].numel <= (int64_t)1 << 42, fi + ": numel out of range");
+        LSN_CHECK_ARG(t[i].dtype == LSN_DT_BF16 || t[i].dtype == LSN_DT_F32, fi + ": unknown type");
+        const uintptr_t es = t[i].dtype == LSN_DT_BF16 ? 2 : 4;
+        if (t[i].numel == 0) continue;
+        LSN_CHECK_ARG(t[i].src != nullptr && (reinterpret_cast<uintptr_t>(t[i].src) % es) == 0, fi + ": src must be aligned to its type");
+        if (clip) {
+            LSN_CHECK_ARG(t[i].dst != nullptr && (reinterpret_cast<uintptr_t>(t[i].dst) % es) == 0, fi + ": dst must be aligned to its type");
+            const uintptr_t a = reinterpret_cast<uintptr_t>(t[i].src), b = reinterpret_cast<uintptr_t>(t[i].dst), k = es * (uintptr_t)t[i].numel;
+            LSN_CHECK_ARG(a == b || a + k <= b || b + k <= a, fi + ": dst overlaps src in part");
+        }
+        chunks += chunks_of(t[i]);
+        bytes += (double)es * (double)t[i].numel * (clip ? 2.0 : 1.0);
+    }
+    LSN_CHECK_ARG(chunks <= INT32_MAX, f + ": too many elements");
+    lsn_status s = check_device();
+    if (s != LSN_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int batches = (int)std::max<int64_t>(1, ceil_div(n, kMaxTensors));
+    TimingScope ts(LSN_K_GRAD, bytes, st, clip ? 2 * batches : batches);
+    GradArgs a;
+    auto fill = [&](int b) {
+        a.n = std::max(1, std::min(n - b * kMaxTensors, kMaxTensors));
+        a.chunks = 0;
+        for (int i = 0; i < a.n; ++i) {
+            const lsn_grad none{};
+            const lsn_grad& q = n == 0 ? none : t[b * kMaxTensors + i];
+            a.src[i] = q.src;
+            a.dst[i] = q.dst;
+            a.numel[i] = (uint64_t)q.numel | (q.dtype == LSN_DT_BF16 ? 1ull << 63 : 0);
+            a.chunk0[i] = a.chunks;
+            a.chunks += (int)chunks_of(q);
+        }
+        return std::max(1, std::min({a.chunks, 8 * sm_count(), kMaxCtas}));
+    };
+    int parts = 0;
+    for (int b = 0; b < batches; ++b) {
+        const int grid = fill(b);
+        s = launch(lsn_grad_norm_kernel, grid, st, a, (GradWs*)ws, parts, parts + grid, b + 1 == batches, max_norm, norm);
+        if (s != LSN_OK) return s;
+        parts += grid;
+    }
+    for (int b = 0; b < batches && clip; ++b) {
+        const int grid = batches == 1 ? std::max(1, std::min({a.chunks, 8 * sm_count(), kMaxCtas})) : fill(b);
+        if ((s = launch(lsn_grad_scale_kernel, grid, st, a, (const GradWs*)ws)) != LSN_OK) return s;
+    }
+    return LSN_OK;
+}
+
+}  // namespace
+
+}  // namespace lsn
+
+using namespace lsn;
+
+extern "C" {
+
+size_t lsn_grad_ws_bytes(int n) { return n < 0 ? 0 : ws_bytes_of(n); }
+
+lsn_status grad_norm(int n, const lsn_grad* t, float* norm, void* ws, size_t ws_bytes, lsn_stream_t stream) {
+    NvtxRange nvtx("grad_norm");
+    return grad_call(n, t, false, 1.f, norm, ws, ws_bytes, stream, "grad_norm");
+}
+
+lsn_status grad_clip(int n, const lsn_grad* t, float max_norm, float* norm, void* ws, size_t ws_bytes, lsn_stream_t stream) {
+    NvtxRange nvtx("grad_clip");
+    return grad_call(n, t, true, max_norm, norm, ws, ws_bytes, stream, "grad_clip");
+}
+
+}  // extern "C"

@@ -1,0 +1,554 @@
+// Sequence log-probabilities and the preference loss, from logits:
+//   lse_t = log sum_v exp l[t, v],   logp_i = sum over scored t of sequence i of (l[t, y_t] - lse_t),
+//   the loss of each pair of sequences from its difference of log ratios, and
+//   dl[t, v] = c_t ([v = y_t] - exp(l[t, v] - lse_t)),   c_t = dloss/dlogp of t's sequence.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "launch.cuh"
+#include "timing.cuh"
+
+namespace lsn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMinSplit = 4096;            // logits of a row that one CTA takes at least
+constexpr int kItems = 148 * 8;            // work items wanted: below as many rows, rows are split
+constexpr size_t kWsHead = 256;
+
+// Pieces a row is cut into, from the shape alone.
+int row_splits(int64_t T, int64_t V) {
+    if (T <= 0) return 1;
+    return (int)std::max<int64_t>(1, std::min(ceil_div(kItems, T), V / kMinSplit));
+}
+
+struct Ws {
+    int done;                              // finished CTAs of the last kernel that counts (zero between calls)
+};
+
+struct Rows {
+    const void* logits;
+    int64_t ld;
+    int T, V, n_seq, splits, average;
+    const int32_t* targets;
+    const int32_t* start;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <class E> struct Words;           // 16-byte words of a row: how many values, and unpacking
+template <> struct Words<uint16_t> {
+    static constexpr int per = 8;
+    static __device__ __forceinline__ void get(const uint4& w, float (&v)[8]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float (&v)[8]) {
+        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+    static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+    static __device__ __forceinline__ void set(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+};
+template <> struct Words<float> {
+    static constexpr int per = 4;
+    static __device__ __forceinline__ void get(const uint4& w, float (&v)[4]) {
+        v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+    static __device__ __forceinline__ float one(const float* p) { return *p; }
+    static __device__ __forceinline__ void set(float* p, float v) { *p = v; }
+};
+
+// Whether row t's target is counted: in the vocabulary, inside the sequences.
+__device__ __forceinline__ bool scored(const Rows& r, int t, int y) {
+    return y >= 0 && y < r.V && t >= r.start[0] && t < r.start[r.n_seq];
+}
+
+// A maximum m and the sum s of exp(x - m), joined with another such pair.
+// m = -infinity stands for "no finite value yet" and subtracts nothing.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    const float at = top == -INFINITY ? 0.f : top;
+    s = s * ex2((m - at) * kLog2e) + s2 * ex2((m2 - at) * kLog2e);
+    m = top;
+}
+
+// First and last full 16-byte word of piece `split` of a row, in words from
+// the row's start rounded down to 16 bytes.
+struct Piece {
+    int w0, w1, mis;
+};
+template <class E>
+__device__ __forceinline__ Piece piece_of(const void* row, int V, int split, int splits) {
+    constexpr int per = Words<E>::per;
+    Piece p;
+    p.mis = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(E);
+    const int first = p.mis ? 1 : 0, end = (V + p.mis) / per;
+    const int64_t n = end > first ? end - first : 0;
+    p.w0 = first + (int)(n * split / splits);
+    p.w1 = first + (int)(n * (split + 1) / splits);
+    return p;
+}
+// Element i (< 2 per) of a row that lies in no full word, or -1.
+template <class E>
+__device__ __forceinline__ int edge_of(int V, int mis, int i) {
+    constexpr int per = Words<E>::per;
+    const int head = mis ? min(per - mis, V) : 0;
+    if (i < head) return i;
+    const int end = max((V + mis) / per * per - mis, head), e = end + i - head;
+    return e < V ? e : -1;
+}
+
+// (m, s) of one piece of one row per work item.  Bound by reading the logits.
+template <class E>
+__global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_constant__ Rows r, float2* part) {
+    constexpr int per = Words<E>::per;
+    constexpr int U = 4;
+    __shared__ float2 sh[kThreads / 32];
+    pdl_wait();
+    const int64_t items = (int64_t)r.T * r.splits;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int t = (int)(it / r.splits), split = (int)(it % r.splits);
+        if (!scored(r, t, r.targets[t])) continue;
+        const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
+        const Piece p = piece_of<E>(row, r.V, split, r.splits);
+        const uint4* words = reinterpret_cast<const uint4*>(row - p.mis);
+        float m = -INFINITY, s = 0.f;
+        for (int w = p.w0 + threadIdx.x; w < p.w1; w += U * kThreads) {
+            float v[U][per];
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (w + u * kThreads < p.w1) {
+                    Words<E>::get(words[w + u * kThreads], v[u]);
+                } else {
+                    #pragma unroll
+                    for (int i = 0; i < per; ++i) v[u][i] = -INFINITY;
+                }
+            }
+            float top = m;
+            #pragma unroll
+            for (int u = 0; u < U; ++u)
+                #pragma unroll
+                for (int i = 0; i < per; ++i) top = fmaxf(top, v[u][i]);
+            const float at = top == -INFINITY ? 0.f : top;
+            s *= ex2((m - at) * kLog2e);
+            m = top;
+            #pragma unroll
+            for (int u = 0; u < U; ++u)
+                #pragma unroll
+                for (int i = 0; i < per; ++i) s += ex2((v[u][i] - at) * kLog2e);
+        }
+        if (split == 0 && threadIdx.x < 2 * per) {
+            const int e = edge_of<E>(r.V, p.mis, threadIdx.x);
+            if (e >= 0) {
+                const float x = Words<E>::one(row + e);
+                join(m, s, x, x == -INFINITY ? 0.f : x - x + 1.f);     // NaN and +infinity give NaN
+            }
+        }
+        #pragma unroll
+        for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(m, s);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kThreads / 32; ++w) join(m, s, sh[w].x, sh[w].y);
+            part[it] = make_float2(m, s);
+        }
+        __syncthreads();
+    }
+}
+
+struct Finish {
+    const float2* part;
+    float* lse;
+    double* logp;
+    int32_t* count;
+    // the loss (pairs of sequences), when wanted
+    int pairs, kind;
+    float beta, smooth, grad_scale;
+    const double* ref;
+    float* reward;
+    float* loss;
+    float* mean;
+    float* dlogp;
+    Ws* ws;
+};
+
+__device__ double block_sum(double v, double* sh) {
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+    #pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) v += sh[w];
+    return v;                              // the sum, in every thread
+}
+
+__device__ __forceinline__ double softplus(double v) { return fmax(v, 0.0) + log1p(exp(-fabs(v))); }
+__device__ __forceinline__ double sigmoid(double v) {
+    const double e = exp(-fabs(v));
+    return v >= 0 ? 1.0 / (1.0 + e) : e / (1.0 + e);
+}
+
+// Loss and its derivative with respect to the difference h of the log ratios.
+__device__ __forceinline__ void pair_loss(const Finish& f, double h, double* loss, double* d) {
+    const double b = f.beta, e = f.smooth, z = b * h;
+    if (f.kind == LSN_PREF_SIGMOID) {
+        // (without smoothing the second term is left out, not multiplied by 0: it may be infinite)
+        *loss = (1.0 - e) * softplus(-z) + (e > 0.0 ? e * softplus(z) : 0.0);
+        *d = b * (e * sigmoid(z) - (1.0 - e) * sigmoid(-z));
+    } else if (f.kind == LSN_PREF_HINGE) {
+        const bool nan = z != z;
+        *loss = nan ? z : fmax(1.0 - z, 0.0);
+        *d = nan ? z : 1.0 - z > 0.0 ? -b : 0.0;
+    } else {
+        const double q = h - 0.5 / b;
+        *loss = q * q;
+        *d = 2.0 * q;
+    }
+}
+
+// One CTA per two sequences (a pair, when there is a loss): the rows' pieces
+// joined into lse, the sequences' sums in fp64 (hundreds of terms that later
+// cancel against the reference's), the loss and its gradients; the last CTA
+// to finish adds the losses up in order.
+template <class E>
+__global__ void __launch_bounds__(kThreads) lsn_seq_finish_kernel(const __grid_constant__ Rows r, const __grid_constant__ Finish f) {
+    __shared__ double sh[kThreads / 32];
+    __shared__ int is_last;
+    pdl_wait();
+    double lp[2] = {0.0, 0.0};
+    int cnt[2] = {1, 1};
+    #pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int q = 2 * blockIdx.x + k;
+        if (q >= r.n_seq) break;
+        const int a = max(r.start[q], 0), b = min(r.start[q + 1], r.T);
+        double sum = 0.0;
+        int n = 0;
+        for (int t = a + threadIdx.x; t < b; t += kThreads) {
+            const int y = r.targets[t];
+            if (!scored(r, t, y)) {
+                f.lse[t] = 0.f;
+                continue;
+            }
+            float m = -INFINITY, s = 0.f;
+            for (int i = 0; i < r.splits; ++i) {
+                const float2 p = f.part[(int64_t)t * r.splits + i];
+                join(m, s, p.x, p.y);
+            }
+            const double ls = log((double)s);
+            const double l = (double)Words<E>::one(reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld + y);
+            f.lse[t] = (float)((double)m + ls);
+            sum += (l - (double)m) - ls;
+            ++n;
+        }
+        sum = block_sum(sum, sh);
+        cnt[k] = max(1, (int)block_sum((double)n, sh));
+        n = (int)block_sum((double)n, sh);
+        lp[k] = r.average ? sum / (double)cnt[k] : sum;
+        if (threadIdx.x == 0) {
+            f.logp[q] = lp[k];
+            if (f.count) f.count[q] = n;
+        }
+    }
+    // rows in no sequence
+    if (blockIdx.x == 0) {
+        for (int t = threadIdx.x; t < min(r.start[0], r.T); t += kThreads) f.lse[t] = 0.f;
+        for (int t = max(r.start[r.n_seq], 0) + threadIdx.x; t < r.T; t += kThreads) f.lse[t] = 0.f;
+    }
+    if (f.pairs == 0) return;
+    if (threadIdx.x == 0) {
+        const int i = blockIdx.x;
+        const double ra = lp[0] - (f.ref ? f.ref[2 * i] : 0.0), rb = lp[1] - (f.ref ? f.ref[2 * i + 1] : 0.0);
+        double loss, d;
+        pair_loss(f, ra - rb, &loss, &d);
+        d *= (double)f.grad_scale / f.pairs;
+        if (f.reward) {
+            f.reward[2 * i] = (float)(f.beta * ra);
+            f.reward[2 * i + 1] = (float)(f.beta * rb);
+        }
+        f.loss[i] = (float)loss;
+        f.dlogp[2 * i] = (float)d;
+        f.dlogp[2 * i + 1] = (float)-d;
+        __threadfence();
+        is_last = f.mean != nullptr && atomicAdd(&f.ws->done, 1) == f.pairs - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!is_last) return;
+    double s = 0.0;
+    for (int i = threadIdx.x; i < f.pairs; i += kThreads) s += (double)__ldcg(&f.loss[i]);
+    s = block_sum(s, sh);
+    if (threadIdx.x == 0) {
+        *f.mean = (float)(s / f.pairs);
+        f.ws->done = 0;
+    }
+}
+
+// The sequence of row t: the last one that starts at or before t.
+__device__ __forceinline__ int seq_of(const Rows& r, int t) {
+    int lo = 0, hi = r.n_seq - 1;
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (r.start[m] <= t) lo = m; else hi = m - 1;
+    }
+    return lo;
+}
+
+// dl = c ([v = y] - exp(l - lse)), zero in rows that are not scored.  Bound by
+// reading the logits and writing their gradient.
+template <class E>
+__global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_constant__ Rows r, const float* lse, const float* dlogp,
+                                                                const int32_t* count, E* dl, int64_t ld_d) {
+    constexpr int per = Words<E>::per;
+    pdl_wait();
+    const int64_t items = (int64_t)r.T * r.splits;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int t = (int)(it / r.splits), split = (int)(it % r.splits);
+        const int y = r.targets[t];
+        const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
+        E* out = dl + (int64_t)t * ld_d;
+        const bool on = scored(r, t, y);
+        float c = 0.f, L = 0.f;
+        if (on) {
+            const int q = seq_of(r, t);
+            c = dlogp[q];
+            if (r.average) c /= (float)max(count[q], 1);
+            L = lse[t];
+        }
+        const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+        if (same) {
+            const Piece p = piece_of<E>(out, r.V, split, r.splits);
+            const uint4* words = reinterpret_cast<const uint4*>(row - p.mis);
+            uint4* outs = reinterpret_cast<uint4*>(out - p.mis);
+            for (int w = p.w0 + threadIdx.x; w < p.w1; w += kThreads) {
+                float v[per];
+                if (on) {
+                    Words<E>::get(words[w], v);
+                    const int e0 = w * per - p.mis;
+                    #pragma unroll
+                    for (int i = 0; i < per; ++i) v[i] = (e0 + i == y ? c : 0.f) - c * ex2((v[i] - L) * kLog2e);
+                } else {
+                    #pragma unroll
+                    for (int i = 0; i < per; ++i) v[i] = 0.f;
+                }
+                outs[w] = Words<E>::put(v);
+            }
+            if (split == 0 && threadIdx.x < 2 * per) {
+                const int e = edge_of<E>(r.V, p.mis, threadIdx.x);
+                if (e >= 0) Words<E>::set(out + e, on ? (e == y ? c : 0.f) - c * ex2((Words<E>::one(row + e) - L) * kLog2e) : 0.f);
+            }
+        } else {
+            const int64_t a = (int64_t)r.V * split / r.splits, b = (int64_t)r.V * (split + 1) / r.splits;
+            for (int64_t e = a + threadIdx.x; e < b; e += kThreads)
+                Words<E>::set(out + e, on ? (e == y ? c : 0.f) - c * ex2((Words<E>::one(row + e) - L) * kLog2e) : 0.f);
+        }
+    }
+}
+
+template <class... P, class... A>
+lsn_status launch(void (*kernel)(P...), int64_t grid, cudaStream_t st, A&&... args) {
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl_attr(at);
+    LSN_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return LSN_OK;
+}
+
+size_t ws_bytes_of(int64_t T, int64_t V) { return kWsHead + round_up((size_t)T * row_splits(T, V) * sizeof(float2), 256); }
+
+bool off_by(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+lsn_status check_in(const lsn_seq_logits* in, const std::string& f) {
+    LSN_CHECK_ARG(in != nullptr, f + ": logits descriptor is NULL");
+    LSN_CHECK_ARG(in->T >= 0 && in->T <= (int64_t)1 << 30, f + ": T out of range");
+    LSN_CHECK_ARG(in->V >= 1 && in->V <= (int64_t)1 << 30, f + ": V out of range");
+    LSN_CHECK_ARG(in->ld >= in->V && in->ld <= (int64_t)1 << 31, f + ": ld must be at least V");
+    LSN_CHECK_ARG(in->dtype == LSN_DT_BF16 || in->dtype == LSN_DT_F32, f + ": unknown type of the logits");
+    LSN_CHECK_ARG(in->n_seq >= 1 && in->n_seq <= 1 << 24, f + ": n_seq out of range");
+    LSN_CHECK_ARG((in->logits && in->targets) || in->T == 0, f + ": NULL tensor");
+    LSN_CHECK_ARG(in->seq_start != nullptr, f + ": seq_start is NULL");
+    LSN_CHECK_ARG(!off_by(in->logits, in->dtype == LSN_DT_BF16 ? 2 : 4), f + ": logits must be aligned to their type");
+    LSN_CHECK_ARG(!off_by(in->targets, 4) && !off_by(in->seq_start, 4), f + ": targets and seq_start must be 4-byte aligned");
+    return LSN_OK;
+}
+
+lsn_status check_ws(const lsn_seq_logits* in, void* ws, size_t ws_bytes, const std::string& f) {
+    LSN_CHECK_ARG(ws != nullptr && aligned16(ws), f + ": workspace must be a 16-byte aligned device pointer");
+    const size_t need = ws_bytes_of(in->T, in->V);
+    LSN_CHECK_ARG(ws_bytes >= need, f + ": workspace too small (need " + std::to_string(need) + " bytes)");
+    return LSN_OK;
+}
+
+lsn_status check_grad(const lsn_seq_logits* in, const float* lse, const float* dlogp, const int32_t* count, const void* dlogits, int64_t ld_d,
+                      const std::string& f) {
+    const size_t es = in->dtype == LSN_DT_BF16 ? 2 : 4;
+    LSN_CHECK_ARG((lse && dlogits) || in->T == 0, f + ": NULL tensor");
+    LSN_CHECK_ARG(dlogp != nullptr, f + ": dlogp is NULL");
+    LSN_CHECK_ARG(count || !in->average, f + ": count is needed for averaged log-probabilities");
+    LSN_CHECK_ARG(ld_d >= in->V && ld_d <= (int64_t)1 << 31, f + ": ld of dlogits must be at least V");
+    LSN_CHECK_ARG(!off_by(dlogits, es), f + ": dlogits must be aligned to its type");
+    if (in->T > 0) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in->logits), b = reinterpret_cast<uintptr_t>(dlogits);
+        const uintptr_t na = es * ((uintptr_t)(in->T - 1) * (uintptr_t)in->ld + (uintptr_t)in->V);
+        const uintptr_t nb = es * ((uintptr_t)(in->T - 1) * (uintptr_t)ld_d + (uintptr_t)in->V);
+        LSN_CHECK_ARG((a == b && ld_d == in->ld) || a + na <= b || b + nb <= a, f + ": dlogits may be the logits themselves or lie apart from them");
+    }
+    return LSN_OK;
+}
+
+Rows rows_of(const lsn_seq_logits* in) {
+    return Rows{in->logits, in->ld, (int)in->T, (int)in->V, in->n_seq, row_splits(in->T, in->V), in->average != 0, in->targets, in->seq_start};
+}
+
+template <class E>
+lsn_status run_fwd(const Rows& r, const Finish& f, float2* part, cudaStream_t st) {
+    if (r.T > 0) {
+        lsn_status s = launch(lsn_seq_stats_kernel<E>, std::min<int64_t>((int64_t)r.T * r.splits, 148 * 8), st, r, part);
+        if (s != LSN_OK) return s;
+    }
+    return launch(lsn_seq_finish_kernel<E>, ceil_div(r.n_seq, 2), st, r, f);
+}
+
+lsn_status fwd(const lsn_seq_logits* in, Finish f, void* ws, cudaStream_t st) {
+    const Rows r = rows_of(in);
+    f.ws = reinterpret_cast<Ws*>(ws);
+    float2* part = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHead);
+    f.part = part;
+    const double es = in->dtype == LSN_DT_BF16 ? 2.0 : 4.0;
+    TimingScope ts(LSN_K_SEQ_LOGP, es * (double)in->T * (double)in->V + 8.0 * (double)in->T, st, 2);
+    return in->dtype == LSN_DT_BF16 ? run_fwd<uint16_t>(r, f, part, st) : run_fwd<float>(r, f, part, st);
+}
+
+lsn_status bwd(const lsn_seq_logits* in, const float* lse, const float* dlogp, const int32_t* count, void* dlogits, int64_t ld_d, cudaStream_t st) {
+    const Rows r = rows_of(in);
+    const int64_t grid = std::min<int64_t>((int64_t)r.T * r.splits, 148 * 8);
+    const double es = in->dtype == LSN_DT_BF16 ? 2.0 : 4.0;
+    TimingScope ts(LSN_K_SEQ_GRAD, 2.0 * es * (double)in->T * (double)in->V, st, 1);
+    return in->dtype == LSN_DT_BF16
+               ? launch(lsn_seq_grad_kernel<uint16_t>, grid, st, r, lse, dlogp, count, (uint16_t*)dlogits, ld_d)
+               : launch(lsn_seq_grad_kernel<float>, grid, st, r, lse, dlogp, count, (float*)dlogits, ld_d);
+}
+
+lsn_status check_loss(const lsn_seq_logits* in, const double* ref, const lsn_preference* p, float* lse, double* logp, int32_t* count, float* reward,
+                      float* loss, float* mean, float* dlogp, const std::string& f) {
+    LSN_CHECK_ARG(p != nullptr, f + ": loss descriptor is NULL");
+    LSN_CHECK_ARG(p->kind == LSN_PREF_SIGMOID || p->kind == LSN_PREF_HINGE || p->kind == LSN_PREF_SQUARED, f + ": unknown loss");
+    LSN_CHECK_ARG(p->beta > 0.f && std::isfinite(p->beta), f + ": beta must be positive and finite");
+    LSN_CHECK_ARG(p->label_smoothing >= 0.f && p->label_smoothing <= 0.5f, f + ": label_smoothing must be in [0, 0.5]");
+    LSN_CHECK_ARG(p->label_smoothing == 0.f || p->kind == LSN_PREF_SIGMOID, f + ": label_smoothing belongs to the sigmoid loss");
+    LSN_CHECK_ARG(std::isfinite(p->grad_scale), f + ": grad_scale must be finite");
+    LSN_CHECK_ARG(in->n_seq % 2 == 0, f + ": sequences come in pairs, one at least");
+    LSN_CHECK_ARG((lse || in->T == 0) && logp && loss && dlogp, f + ": NULL tensor");
+    LSN_CHECK_ARG(!off_by(lse, 4) && !off_by(logp, 8) && !off_by(ref, 8) && !off_by(count, 4) && !off_by(reward, 4) && !off_by(loss, 4) &&
+                      !off_by(mean, 4) && !off_by(dlogp, 4), f + ": tensors must be aligned to their types");
+    return LSN_OK;
+}
+
+Finish finish_of(const lsn_seq_logits* in, const double* ref, const lsn_preference* p, float* lse, double* logp, int32_t* count, float* reward, float* loss,
+                 float* mean, float* dlogp) {
+    Finish f{};
+    f.lse = lse;
+    f.logp = logp;
+    f.count = count;
+    f.pairs = in->n_seq / 2;
+    f.kind = p->kind;
+    f.beta = p->beta;
+    f.smooth = p->label_smoothing;
+    f.grad_scale = p->grad_scale;
+    f.ref = ref;
+    f.reward = reward;
+    f.loss = loss;
+    f.mean = mean;
+    f.dlogp = dlogp;
+    return f;
+}
+
+}  // namespace
+
+}  // namespace lsn
+
+using namespace lsn;
+
+extern "C" {
+
+size_t lsn_seq_logp_ws_bytes(const lsn_seq_logits* in) {
+    if (in == nullptr || in->T < 0 || in->T > (int64_t)1 << 30 || in->V < 1 || in->V > (int64_t)1 << 30) return 0;
+    return ws_bytes_of(in->T, in->V);
+}
+
+lsn_status seq_logp_fwd(const lsn_seq_logits* in, float* lse, double* logp, int32_t* count, void* ws, size_t ws_bytes, lsn_stream_t stream) {
+    NvtxRange nvtx("seq_logp_fwd");
+    lsn_status s = check_in(in, "seq_logp_fwd");
+    if (s != LSN_OK) return s;
+    LSN_CHECK_ARG((lse || in->T == 0) && logp, "seq_logp_fwd: NULL tensor");
+    LSN_CHECK_ARG(!off_by(lse, 4) && !off_by(logp, 8) && !off_by(count, 4), "seq_logp_fwd: tensors must be aligned to their types");
+    if ((s = check_ws(in, ws, ws_bytes, "seq_logp_fwd")) != LSN_OK) return s;
+    if ((s = check_device()) != LSN_OK) return s;
+    Finish f{};
+    f.lse = lse;
+    f.logp = logp;
+    f.count = count;
+    return fwd(in, f, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lsn_status seq_logp_bwd(const lsn_seq_logits* in, const float* lse, const float* dlogp, const int32_t* count, void* dlogits, int64_t ld_d,
+                        lsn_stream_t stream) {
+    NvtxRange nvtx("seq_logp_bwd");
+    lsn_status s = check_in(in, "seq_logp_bwd");
+    if (s != LSN_OK) return s;
+    if (in->T == 0) return LSN_OK;
+    if ((s = check_grad(in, lse, dlogp, count, dlogits, ld_d, "seq_logp_bwd")) != LSN_OK) return s;
+    LSN_CHECK_ARG(!off_by(lse, 4) && !off_by(dlogp, 4) && !off_by(count, 4), "seq_logp_bwd: tensors must be aligned to their types");
+    if ((s = check_device()) != LSN_OK) return s;
+    return bwd(in, lse, dlogp, count, dlogits, ld_d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lsn_status preference_loss_fwd(const lsn_seq_logits* in, const double* ref_logp, const lsn_preference* p, float* lse, double* logp, int32_t* count,
+                               float* reward, float* loss, float* mean_loss, float* dlogp, void* ws, size_t ws_bytes, lsn_stream_t stream) {
+    NvtxRange nvtx("preference_loss_fwd");
+    lsn_status s = check_in(in, "preference_loss_fwd");
+    if (s != LSN_OK) return s;
+    if ((s = check_loss(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp, "preference_loss_fwd")) != LSN_OK) return s;
+    if ((s = check_ws(in, ws, ws_bytes, "preference_loss_fwd")) != LSN_OK) return s;
+    if ((s = check_device()) != LSN_OK) return s;
+    return fwd(in, finish_of(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp), ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lsn_status preference_loss_fwd_bwd(const lsn_seq_logits* in, const double* ref_logp, const lsn_preference* p, float* lse, double* logp, int32_t* count,
+                                   float* reward, float* loss, float* mean_loss, float* dlogp, void* dlogits, int64_t ld_d, void* ws, size_t ws_bytes,
+                                   lsn_stream_t stream) {
+    NvtxRange nvtx("preference_loss_fwd_bwd");
+    const char* who = "preference_loss_fwd_bwd";
+    lsn_status s = check_in(in, who);
+    if (s != LSN_OK) return s;
+    if ((s = check_loss(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp, who)) != LSN_OK) return s;
+    if ((s = check_grad(in, lse, dlogp, count, dlogits, ld_d, who)) != LSN_OK) return s;
+    if ((s = check_ws(in, ws, ws_bytes, who)) != LSN_OK) return s;
+    if ((s = check_device()) != LSN_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((s = fwd(in, finish_of(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp), ws, st)) != LSN_OK) return s;
+    if (in->T == 0) return LSN_OK;
+    return bwd(in, lse, dlogp, count, dlogits, ld_d, st);
+}
+
+}  // extern "C"

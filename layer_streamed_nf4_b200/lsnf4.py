@@ -52,6 +52,8 @@ EXPORTS = (
     "lsn_layer_ws_bytes", "lora_layer_fwd", "lora_layer_bwd", "nf4_dequant_batch",
     "lsn_selftest_wait_timeout", "layer_pool_set_debug",
     "lsn_decode_ws_bytes", "lora_linear_decode", "lora_layer_decode",
+    "lsn_seq_logp_ws_bytes", "seq_logp_fwd", "seq_logp_bwd", "preference_loss_fwd", "preference_loss_fwd_bwd",
+    "lsn_grad_ws_bytes", "grad_norm", "grad_clip",
 )
 
 
@@ -78,9 +80,31 @@ class LoraProj(ctypes.Structure):
                 ("dB", ctypes.c_void_p), ("u", ctypes.c_void_p), ("group", ctypes.c_int)]
 
 
-LSN_LAYER_MAX_PROJ = 16
+class SeqLogits(ctypes.Structure):
+    """Logits of a packed batch of sequences with their targets (lsn_seq_logits)."""
+    _fields_ = [("logits", ctypes.c_void_p), ("T", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("targets", ctypes.c_void_p), ("n_seq", ctypes.c_int),
+                ("seq_start", ctypes.c_void_p), ("average", ctypes.c_int)]
 
-KERNEL_KINDS = ("gemm_fwd", "gemm_bwd", "dequant", "lora_down", "lora_tgrad", "quantize", "decode")
+
+class Preference(ctypes.Structure):
+    """A preference loss (lsn_preference)."""
+    _fields_ = [("kind", ctypes.c_int), ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float),
+                ("grad_scale", ctypes.c_float)]
+
+
+class Grad(ctypes.Structure):
+    """One gradient tensor of a norm or clip call (lsn_grad)."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
+
+
+LSN_LAYER_MAX_PROJ = 16
+LSN_DT_BF16, LSN_DT_F32 = 0, 1
+LSN_PREF_SIGMOID, LSN_PREF_HINGE, LSN_PREF_SQUARED = 0, 1, 2
+
+KERNEL_KINDS = ("gemm_fwd", "gemm_bwd", "dequant", "lora_down", "lora_tgrad", "quantize", "decode", "seq_logp",
+                "seq_grad", "grad")
 _NK = len(KERNEL_KINDS)
 
 
@@ -128,6 +152,15 @@ _sig("lora_layer_bwd", _i, [_i, ctypes.POINTER(LoraProj), _i64, _i, ctypes.c_flo
 _sig("lsn_decode_ws_bytes", _sz, [_i, ctypes.POINTER(LoraProj), _i64, _i])
 _sig("lora_linear_decode", _i, [ctypes.POINTER(Base), _vp, _i64, _vp, _vp, _i, ctypes.c_float, _vp, _vp, _sz, _vp])
 _sig("lora_layer_decode", _i, [_i, ctypes.POINTER(LoraProj), _i64, _i, ctypes.c_float, _vp, _sz, _vp])
+_sig("lsn_seq_logp_ws_bytes", _sz, [ctypes.POINTER(SeqLogits)])
+_sig("seq_logp_fwd", _i, [ctypes.POINTER(SeqLogits), _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("seq_logp_bwd", _i, [ctypes.POINTER(SeqLogits), _vp, _vp, _vp, _vp, _i64, _vp])
+_sig("preference_loss_fwd", _i, [ctypes.POINTER(SeqLogits), _vp, ctypes.POINTER(Preference)] + [_vp] * 8 + [_sz, _vp])
+_sig("preference_loss_fwd_bwd", _i, [ctypes.POINTER(SeqLogits), _vp, ctypes.POINTER(Preference)] + [_vp] * 8 +
+     [_i64, _vp, _sz, _vp])
+_sig("lsn_grad_ws_bytes", _sz, [_i])
+_sig("grad_norm", _i, [_i, ctypes.POINTER(Grad), _vp, _vp, _sz, _vp])
+_sig("grad_clip", _i, [_i, ctypes.POINTER(Grad), ctypes.c_float, _vp, _vp, _sz, _vp])
 _sig("lsn_set_option", _i, [_i, _i])
 _sig("lsn_get_option", _i, [_i])
 _IP = ctypes.POINTER(ctypes.c_int)
@@ -318,6 +351,78 @@ def lora_layer_decode(projs, T: int, r: int, scale: float, ws, ws_bytes: int, st
     arr = projs if isinstance(projs, ctypes.Array) else proj_array(projs)
     _check(_lib.lora_layer_decode(len(arr), arr, T, r, scale, _ptr(ws), ws_bytes, _stream(stream)),
            "lora_layer_decode")
+
+
+# ------------------------------------------------------ preference loss ---
+
+def seq_logits(logits, T: int, V: int, ld: int, dtype: int, targets, n_seq: int, seq_start,
+               average: bool = False) -> SeqLogits:
+    """Logits [T, V] (row stride ld), int32 targets [T] and int32 seq_start [n_seq + 1], all on the device; keep the
+    tensors alive while the descriptor is used."""
+    return SeqLogits(_ptr(logits), T, V, ld, dtype, _ptr(targets), n_seq, _ptr(seq_start), int(bool(average)))
+
+
+def preference(kind: int, beta: float, label_smoothing: float = 0.0, grad_scale: float = 1.0) -> Preference:
+    return Preference(kind, beta, label_smoothing, grad_scale)
+
+
+def seq_logp_ws_bytes(sl: SeqLogits) -> int:
+    return _lib.lsn_seq_logp_ws_bytes(ctypes.byref(sl))
+
+
+def seq_logp_fwd(sl: SeqLogits, lse, logp, count, ws, ws_bytes: int, stream=None):
+    """lse fp32 [T], logp fp64 [n_seq] and (or None) count int32 [n_seq] of a batch of sequences."""
+    _check(_lib.seq_logp_fwd(ctypes.byref(sl), _ptr(lse), _ptr(logp), _ptr(count), _ptr(ws), ws_bytes,
+                             _stream(stream)), "seq_logp_fwd")
+
+
+def seq_logp_bwd(sl: SeqLogits, lse, dlogp, count, dlogits, ld_d: int, stream=None):
+    _check(_lib.seq_logp_bwd(ctypes.byref(sl), _ptr(lse), _ptr(dlogp), _ptr(count), _ptr(dlogits), ld_d,
+                             _stream(stream)), "seq_logp_bwd")
+
+
+def preference_loss_fwd(sl: SeqLogits, ref_logp, p: Preference, lse, logp, count, reward, loss, mean_loss, dlogp, ws,
+                        ws_bytes: int, stream=None):
+    _check(_lib.preference_loss_fwd(ctypes.byref(sl), _ptr(ref_logp), ctypes.byref(p), _ptr(lse), _ptr(logp),
+                                    _ptr(count), _ptr(reward), _ptr(loss), _ptr(mean_loss), _ptr(dlogp), _ptr(ws),
+                                    ws_bytes, _stream(stream)), "preference_loss_fwd")
+
+
+def preference_loss_fwd_bwd(sl: SeqLogits, ref_logp, p: Preference, lse, logp, count, reward, loss, mean_loss, dlogp,
+                            dlogits, ld_d: int, ws, ws_bytes: int, stream=None):
+    _check(_lib.preference_loss_fwd_bwd(ctypes.byref(sl), _ptr(ref_logp), ctypes.byref(p), _ptr(lse), _ptr(logp),
+                                        _ptr(count), _ptr(reward), _ptr(loss), _ptr(mean_loss), _ptr(dlogp),
+                                        _ptr(dlogits), ld_d, _ptr(ws), ws_bytes, _stream(stream)),
+           "preference_loss_fwd_bwd")
+
+
+# -------------------------------------------- gradient norm and clipping ---
+
+def grad_tensor(src, numel: int, dtype: int, dst=None) -> Grad:
+    """One gradient of a norm or clip call; dst None: clipped in place."""
+    return Grad(_ptr(src), _ptr(src) if dst is None else _ptr(dst), numel, dtype)
+
+
+def grad_array(tensors) -> ctypes.Array:
+    return (Grad * len(tensors))(*tensors)
+
+
+def _grads(tensors):
+    return tensors if isinstance(tensors, ctypes.Array) else grad_array(tensors)
+
+
+def grad_ws_bytes(tensors) -> int:
+    return _lib.lsn_grad_ws_bytes(len(tensors))
+
+
+def grad_norm(tensors, norm, ws, ws_bytes: int, stream=None):
+    arr = _grads(tensors)
+    _check(_lib.grad_norm(len(arr), arr, _ptr(norm), _ptr(ws), ws_bytes, _stream(stream)), "grad_norm")
+
+
+def grad_clip(tensors, max_norm: float, norm, ws, ws_bytes: int, stream=None):
+    arr = _grads(tensors)
+    _check(_lib.grad_clip(len(arr), arr, max_norm, _ptr(norm), _ptr(ws), ws_bytes, _stream(stream)), "grad_clip")
 
 
 def selftest_wait_timeout(limit_us: int = 1000, stream=None) -> int:
