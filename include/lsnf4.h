@@ -311,8 +311,9 @@ lsn_status lora_layer_bwd(int n, const lsn_lora_proj* p, int64_t T, int r, float
 #define LSN_DECODE_MAX_T 16
 
 /* Workspace bytes of lora_linear_decode (n = 1) and lora_layer_decode for these
- * projections, at most T tokens and this rank (0 when an argument is invalid).
- * It need not be zeroed. */
+ * projections, T tokens and this rank (0 when an argument is invalid).  It
+ * starts with the kernels' status word (lsn_ws_status): zero-fill a new
+ * workspace once. */
 size_t lsn_decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r);
 
 lsn_status lora_linear_decode(const lsn_base* W, const uint16_t* x, int64_t T, const uint16_t* A, const uint16_t* B,

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -14,29 +15,47 @@ namespace lsn {
 
 namespace {
 
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 512;
 constexpr int kPrepWarps = kPrepThreads / 32;
 constexpr int kPrepCtas = 8;       // CTAs (one cluster) that share the contraction of one projection's u
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 32;          // output rows of a tile: two 16-row MMA operands per warp
-constexpr int kTableBytes = 65536;
+constexpr int kRows = 32;          // output rows of a warp's tile: two 16-row MMA operands
+constexpr int kStageBlocks = 4;    // blocks of 64 codes in a stage: 128 bytes of each row
+constexpr int kStageBytes = kRows * kStageBlocks * 32;
+constexpr int kDepth = 2;          // stages of a warp in flight
+constexpr int kMaxGrid = 148;
+
+// Shared memory, in addresses of the shared window: the lookup table at 64 KB,
+// so that an entry's address is its 16 low bits or-ed with a constant; the
+// rings of the first 7 warps below it, the others' and the rest above.
+constexpr uint32_t kTableAt = 0x10000, kTableEnd = 0x20000;
+constexpr uint32_t kRingBytes = kDepth * kStageBytes;                  // of a warp
+constexpr int kRingsBelow = 7;
+constexpr uint32_t kBelowAt = kTableAt - kRingsBelow * kRingBytes;     // also the highest start of the block's memory
+constexpr uint32_t kAmAt = kTableEnd + (kWarps - kRingsBelow) * kRingBytes;
+constexpr uint32_t kBarAt = kAmAt + kWarps * kRows * kStageBlocks * 4;
+constexpr uint32_t kSmem = kBarAt + kWarps * kDepth * 8 - 1024;        // the window's first KB is the system's
 
 struct PrepProj {
     const uint16_t* x;
     const uint16_t* A;      // NULL: adapter off
     float* u;               // [T, r]
-    __half* xf;             // [K/64, T, 64] fp16, or NULL when another projection lays the same x out
-    float* xs;              // [K/64, 8 NT] scale of each fp16 block
+    __half* xf;             // [K/64, 2, TP, 32] fp16, or NULL when another projection lays the same x out
+    float* xs;              // [K/64, TP] scale of each fp16 block
     int nb;                 // K / 64
 };
 struct PrepArgs {
     PrepProj p[LSN_LAYER_MAX_PROJ];
+    int* counters;          // zeroed for lsn_decode_kernel
+    int n_counters;
     int T, r;
 };
 
+// The work of a projection in CTA steps: a step is one stage (4 blocks along
+// K) for each of the CTA's 16 warps, G row groups of 32 rows times W = 16 / G
+// stages along K.  Tiles of G row groups take `steps` steps each.
 struct DecodeProj {
-    const uint8_t* packed;
     const uint8_t* q;
     const float* s2;
     const float* offset;
@@ -46,12 +65,21 @@ struct DecodeProj {
     const uint16_t* B;
     uint16_t* y;
     int nb, N;
-    int tile0;              // number of this projection's first tile
+    int log_g;              // G = 1 << log_g
+    int steps, tiles, stages;   // stages: along K
+    int counter0;           // its first counter
+    int q_align;            // rows of q start on multiples of 4, 2 or 1 bytes
 };
 struct DecodeArgs {
-    DecodeProj p[LSN_LAYER_MAX_PROJ];
+    CUtensorMap map[LSN_LAYER_MAX_PROJ];
+    int step0[LSN_LAYER_MAX_PROJ];      // first step of each projection (beyond the last: INT_MAX)
     float level[16];
-    int n, T, r, tiles;
+    DecodeProj p[LSN_LAYER_MAX_PROJ];
+    int* err;
+    int* counters;          // one per row group and warp share of it
+    float* part;            // [grid, 2][16 warps][8 NT][32] partial sums
+    int n, T, r;
+    int per, rem;           // steps of a CTA
     float scale;
 };
 
@@ -61,7 +89,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -91,7 +119,7 @@ __device__ __forceinline__ X16 load16(const uint16_t* p, bool on) {
 // 2^-24 of 2^-14 of the largest, below what an fp32 sum keeps; the power of
 // two puts the largest finite value into [2^14, 2^15).  Infinities and NaN
 // stay what they are.
-__device__ __forceinline__ void lay_out_x(const X16& v, bool on, __half* dst, float* xs, int t4) {
+__device__ __forceinline__ void lay_out_x(const X16& v, bool on, bool slot, __half* dst, int half, float* xs, int t4) {
     uint32_t top = 0;
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -113,23 +141,26 @@ __device__ __forceinline__ void lay_out_x(const X16& v, bool on, __half* dst, fl
         h[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
     if (on) {
-        uint4* d = reinterpret_cast<uint4*>(dst);
-        d[0] = make_uint4(h[0], h[1], h[2], h[3]);
-        d[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(dst + half) = make_uint4(h[4], h[5], h[6], h[7]);
     }
-    if (t4 == 0) *xs = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+    if (slot && t4 == 0) *xs = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }
 
 // u = x A^T for 16 rows of A (blockIdx.y) of one projection (blockIdx.z), the
 // blocks of 64 along K shared out over the cluster's CTAs and their warps,
 // and x laid out for lsn_decode_kernel.  Sums in fp32: MMA accumulators, then
 // the warps in order, then the cluster's CTAs in order.
-template <int NT>
+template <int TP>
 __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __grid_constant__ PrepArgs args) {
+    constexpr int NT = (TP + 7) / 8;
     __shared__ float part[kPrepWarps][16][8 * NT];
     __shared__ float mine[16][8 * NT];
     pdl_wait();
     pdl_launch_dependents();
+    for (int i = ((blockIdx.z * gridDim.y + blockIdx.y) * kPrepCtas + blockIdx.x) * kPrepThreads + threadIdx.x; i < args.n_counters;
+         i += gridDim.z * gridDim.y * kPrepCtas * kPrepThreads)
+        args.counters[i] = 0;
     const PrepProj& p = args.p[blockIdx.z];
     const int T = args.T, r = args.r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -159,7 +190,7 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
                 for (int i = 0; i < NT; ++i) {
                     const int t = g + 8 * i;
                     // absent tokens (all zeros) take part in the shuffles and leave a scale that multiplies zeros
-                    lay_out_x(xv[i], t < T, p.xf + ((int64_t)b * T + t) * 64 + 16 * t4, p.xs + (int64_t)b * 8 * NT + t, t4);
+                    lay_out_x(xv[i], t < T, t < TP, p.xf + ((int64_t)b * 2 * TP + t) * 32 + 8 * t4, TP * 32, p.xs + (int64_t)b * TP + t, t4);
                 }
             }
         }
@@ -199,114 +230,501 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
 
 extern __shared__ __align__(1024) uint8_t smem_raw[];
 
-// One 32-row tile of one projection at a time: each warp takes every 16th
-// block of 64 along K of all 32 rows, so a warp's x registers serve two MMA
-// row groups; the warps' partial sums meet in shared memory.
-template <int NT>
+// First step of CTA c, and the CTA that has step s: the first `rem` CTAs take
+// one step more than the others' `per`.
+__device__ __forceinline__ int first_step(const DecodeArgs& a, int c) { return c * a.per + min(c, a.rem); }
+__device__ __forceinline__ int cta_of(const DecodeArgs& a, int s) {
+    const unsigned cut = (unsigned)a.rem * (unsigned)(a.per + 1);
+    return (unsigned)s < cut ? (unsigned)s / (unsigned)(a.per + 1) : a.rem + ((unsigned)s - cut) / (unsigned)a.per;
+}
+
+// A warp's walk over its stages of the CTA's steps: the projection and tile
+// it is in, and within the tile one stage every W.
+struct Walk {
+    int left;            // steps of the CTA still to come, this tile's included
+    int here;            // of those, steps of this tile
+    int p, tile;
+    int ks, dks;         // this step's stage, and the distance to the next step's
+    int stages;          // stages of this tile's rows for this warp (0: it has no rows here)
+    int rg;
+
+    __device__ __forceinline__ void enter(const DecodeArgs& a, int warp, int step) {
+        const DecodeProj& q = a.p[p];
+        const int lg = q.log_g;
+        rg = (tile << lg) + (warp & ((1 << lg) - 1));
+        dks = kWarps >> lg;
+        ks = step * dks + (warp >> lg);
+        stages = rg * kRows < q.N ? q.stages : 0;
+        here = min(left, q.steps - step);
+    }
+    __device__ void start(const DecodeArgs& a, int warp, int s0, int s1) {
+        left = s1 - s0;
+        p = 0;
+        #pragma unroll
+        for (int i = 1; i < LSN_LAYER_MAX_PROJ; ++i) p += s0 >= a.step0[i];
+        const int local = s0 - a.step0[p];
+        tile = local / a.p[p].steps;
+        enter(a, warp, local - tile * a.p[p].steps);
+    }
+    __device__ __forceinline__ void next_tile(const DecodeArgs& a, int warp) {
+        if (++tile == a.p[p].tiles) {
+            tile = 0;
+            ++p;
+        }
+        enter(a, warp, 0);
+    }
+};
+
+// The same for the loads, with the lane's row of the second-level codes.
+struct LoadWalk : Walk {
+    const uint8_t* q;
+    const float* s2;
+    uint32_t at0;        // number of the row's first block (< 2^32: checked at launch)
+    int nb, align;
+
+    __device__ __forceinline__ void rows(const DecodeArgs& a, int lane) {
+        const DecodeProj& d = a.p[p];
+        nb = d.nb;
+        align = d.q_align;
+        at0 = (uint32_t)(rg * kRows + lane) * (uint32_t)nb;
+        q = d.q + at0;
+        s2 = d.s2;
+    }
+};
+
+// absmax = offset + table[q] s2 with table[q] = (q - 127) / 127, [255] = 0, of
+// the four blocks of a stage; blocks from `cut` on belong to the next group's s2.
+struct AmRaw {
+    uint32_t q;
+    float s2a, s2b;
+    int cut;
+};
+__device__ __forceinline__ AmRaw load_am(const LoadWalk& w, int ks) {
+    AmRaw r;
+    const int b0 = ks * kStageBlocks;
+    const uint32_t at = w.at0 + (uint32_t)b0;
+    const uint8_t* q = w.q + b0;
+    r.cut = kStageBlocks;
+    r.s2a = r.s2b = w.s2[at >> 8];
+    if (w.align == 4) {                         // nb % 4 == 0: four blocks, all of one group
+        r.q = *reinterpret_cast<const uint32_t*>(q);
+        return r;
+    }
+    const int n = min(kStageBlocks, w.nb - b0);
+    if (w.align == 2) {                         // nb % 2 == 0: n is 2 or 4
+        r.q = *reinterpret_cast<const uint16_t*>(q);
+        if (n > 2) r.q |= (uint32_t)*reinterpret_cast<const uint16_t*>(q + 2) << 16;
+    } else {
+        r.q = q[0];
+        if (n > 1) r.q |= (uint32_t)q[1] << 8;
+        if (n > 2) r.q |= (uint32_t)q[2] << 16;
+        if (n > 3) r.q |= (uint32_t)q[3] << 24;
+    }
+    r.cut = 256 - (int)(at & 255u);
+    if (r.cut < n) r.s2b = w.s2[(at >> 8) + 1];
+    return r;
+}
+__device__ __forceinline__ float4 absmax4(const AmRaw& r, float offset) {
+    uint32_t q = r.q;
+    if (((q & 0x7f7f7f7fu) + 0x01010101u) & q & 0x80808080u) {  // a byte is 255: it stands for 0, as 127 does
+        const uint32_t ff = __vcmpeq4(q, 0xffffffffu);
+        q = (q & ~ff) | (0x7f7f7f7fu & ff);
+    }
+    const float ka = r.s2a * (1.f / 127.f), kb = r.s2b * (1.f / 127.f);
+    const float oa = offset - r.s2a, ob = offset - r.s2b;
+    float4 v;
+    v.x = fmaf((float)(q & 255u), ka, oa);
+    v.y = fmaf((float)((q >> 8) & 255u), r.cut > 1 ? ka : kb, r.cut > 1 ? oa : ob);
+    v.z = fmaf((float)((q >> 16) & 255u), r.cut > 2 ? ka : kb, r.cut > 2 ? oa : ob);
+    v.w = fmaf((float)(q >> 24), r.cut > 3 ? ka : kb, r.cut > 3 ? oa : ob);
+    return v;
+}
+
+// Shared memory by its 32-bit address.
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ldsf(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void stsf(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+
+__device__ __forceinline__ void stsf4(uint32_t a, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// The table's entry for byte I of w, in this lane's copy: its address is
+// kTableAt | byte << 8 | lane * 4, one byte permute.
+template <int I>
+__device__ __forceinline__ uint32_t lookup(uint32_t w, uint32_t lane4) {
+    uint32_t v;
+    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(prmt(w, lane4, 0x7604u | (uint32_t)I << 4)));
+    return v;
+}
+// The four A registers of an MMA: bytes k and k + 1 of a word of the rows 0-7 (u) and 8-15 (v).
+template <int K>
+__device__ __forceinline__ void operand(uint32_t (&a)[4], uint32_t u, uint32_t v, uint32_t lane4) {
+    a[0] = lookup<K>(u, lane4);
+    a[1] = lookup<K>(v, lane4);
+    a[2] = lookup<K + 1>(u, lane4);
+    a[3] = lookup<K + 1>(v, lane4);
+}
+
+// Row of MMA operand row g (0..7) within 8 where lanes read 8 bytes: the lanes of half a warp take even
+// (odd) rows, whose 16-byte pieces the 128-byte swizzle puts into different banks.
+__device__ __forceinline__ int row_of(int g) { return g < 4 ? 2 * g : 2 * g - 7; }
+
+// The adapter's term of a warp's tile, s u B^T, added to its sums.  TP == 2:
+// the lanes of a quad, whose sums are added up afterwards, take a quarter of
+// the rank each; otherwise each lane has its own tokens.
+template <int TP, int NT>
+__device__ __forceinline__ void add_adapter(const DecodeArgs& a, const DecodeProj& p, int row, int t4, float (&acc)[2][NT][4]) {
+    const int r = a.r, T = a.T;
+    if constexpr (TP == 2) {
+        for (int j = 2 * t4; j < r; j += 8) {
+            uint32_t b[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const uint32_t*>(p.B + (int64_t)(row + 8 * i) * r + j);
+            #pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t >= T) break;
+                const float2 u = *reinterpret_cast<const float2*>(p.u + t * r + j);
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float d = fmaf(u.x, __uint_as_float(b[i] << 16), u.y * __uint_as_float(b[i] & 0xffff0000u));
+                    acc[i / 2][0][2 * (i & 1) + t] = fmaf(a.scale, d, acc[i / 2][0][2 * (i & 1) + t]);
+                }
+            }
+        }
+    } else {
+        for (int j = 0; j < r; j += 4) {
+            uint2 b[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const uint2*>(p.B + (int64_t)(row + 8 * i) * r + j);
+            #pragma unroll
+            for (int k = 0; k < 2 * NT; ++k) {
+                const int t = 8 * (k / 2) + 2 * t4 + (k & 1);
+                if (t >= T) continue;
+                const float4 u = *reinterpret_cast<const float4*>(p.u + t * r + j);
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float d = u.x * __uint_as_float(b[i].x << 16);
+                    d = fmaf(u.y, __uint_as_float(b[i].x & 0xffff0000u), d);
+                    d = fmaf(u.z, __uint_as_float(b[i].y << 16), d);
+                    d = fmaf(u.w, __uint_as_float(b[i].y & 0xffff0000u), d);
+                    float& s = acc[i / 2][k / 2][2 * (i & 1) + (k & 1)];
+                    s = fmaf(a.scale, d, s);
+                }
+            }
+        }
+    }
+}
+
+// Persistent: every CTA takes an equal, contiguous share of the steps of all
+// projections.  Each warp streams its own stages (32 rows x 128 bytes) through
+// a ring of TMA copies, looks every pair of codes up in the table and
+// multiplies on the tensor cores; nothing is shared between the warps until a
+// tile's sums are complete.  A tile
+// cut between CTAs is added up by the CTA that finishes it last, in the order
+// of the CTAs.
+//
+// TP is the padded token count.  8 or 16: the MMA's columns are tokens, and
+// each block of 64 is scaled by its absmax after its four MMAs.  2: a column
+// is (block of the stage, token), B being zero in the columns of other blocks;
+// a stage's 16 MMAs then accumulate into one set of sums, scaled together at
+// its end, each lane its own block.
+template <int TP>
 __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_constant__ DecodeArgs args) {
     // entry e of the table: the levels of byte e's two codes (high nibble
     // first) as fp16, once for each lane (256 bytes apart), so that a warp's
-    // lookups never meet in a bank and an entry's address is a byte permute
-    float* const part = reinterpret_cast<float*>(smem_raw + kTableBytes);   // [warp][row][token]
+    // lookups never meet in a bank.  The second 128 bytes of an entry hold
+    // sums on their way between warps.
+    constexpr int NT = (TP + 7) / 8;
+    constexpr int Q = 8 * NT;           // sums per lane
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int T = args.T, r = args.r;
-    for (int e = warp; e < 256; e += kWarps) {
-        const __half2 h = __floats2half2_rn(args.level[e >> 4], args.level[e & 15]);
-        *reinterpret_cast<__half2*>(smem_raw + e * 256 + lane * 4) = h;
+    uint8_t* const window = smem_raw - smem_u32(smem_raw);              // address 0 of the shared window
+    const uint32_t ring = (warp < kRingsBelow ? kBelowAt + warp * kRingBytes : kTableEnd + (warp - kRingsBelow) * kRingBytes);
+    const uint32_t am_sh = kAmAt + warp * kRows * kStageBlocks * 4;
+    uint64_t* const full = reinterpret_cast<uint64_t*>(window + kBarAt) + warp * kDepth;
+    if (smem_u32(smem_raw) < 1024 || smem_u32(smem_raw) > kBelowAt) {   // the layout does not fit this window
+        if (threadIdx.x == 0) atomicExch(args.err, 2);
+        return;
+    }
+    const int T = args.T;
+    const int begin = first_step(args, blockIdx.x), end = first_step(args, blockIdx.x + 1);
+    const int rowp = row_of(g);
+
+    if (lane == 0) {
+        for (int i = 0; i < kDepth; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+
+    // the codes and their scales are not written by the kernel before this one
+    // on the stream, which itself began after everything older was complete:
+    // they are read ahead of pdl_wait
+    LoadWalk ld;
+    ld.start(args, warp, begin, end);
+    ld.rows(args, lane);
+    AmRaw raw[kDepth];
+    int issued = 0;
+    auto load_next = [&](AmRaw& out) {
+        while (ld.left > 0) {
+            if (ld.here == 0) {
+                ld.next_tile(args, warp);
+                ld.rows(args, lane);
+            }
+            const int ks = ld.ks;
+            --ld.left;
+            --ld.here;
+            ld.ks += ld.dks;
+            if (ks >= ld.stages) continue;
+            if (lane == 0) {
+                uint64_t* bar = &full[issued % kDepth];
+                mbar_arrive_expect_tx(bar, kStageBytes);
+                tma_load_2d(window + ring + (issued % kDepth) * kStageBytes, &args.map[ld.p], ks * 64, ld.rg * kRows, bar);
+            }
+            out = load_am(ld, ks);
+            ++issued;
+            return;
+        }
+    };
+    #pragma unroll
+    for (int i = 0; i < kDepth; ++i) load_next(raw[i]);
+
+    {   // warp w makes entries 16 w .. 16 w + 15: the high code's level is its own
+        const float lv = args.level[lane & 15], hi = __shfl_sync(0xffffffffu, lv, warp);
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __half2 h = __floats2half2_rn(hi, __shfl_sync(0xffffffffu, lv, i));
+            *reinterpret_cast<__half2*>(window + kTableAt + (warp * 16 + i) * 256 + lane * 4) = h;
+        }
     }
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    const uint32_t lane4 = lane * 4;
+    const uint32_t lane4 = kTableAt | lane * 4;
+    // this lane's first piece of a row in a stage, in the 128-byte swizzle.
+    // the 8 bytes that are t4's of block 0 (block j: xor 32 j)
+    const uint32_t piece = rowp * 128 + ((t4 >> 1) ^ rowp) * 16 + (t4 & 1) * 8;
 
-    int pi = 0;
-    for (int tile = blockIdx.x; tile < args.tiles; tile += gridDim.x) {
-        while (pi + 1 < args.n && tile >= args.p[pi + 1].tile0) ++pi;
-        const DecodeProj& p = args.p[pi];
-        const int n0 = (tile - p.tile0) * kRows;
-        const int nb = p.nb;
+    int used = 0;
+    bool dead = false;
+    Walk cur;
+    cur.start(args, warp, begin, end);
+    while (cur.left > 0) {
+        const DecodeProj& p = args.p[cur.p];
+        const int tile = cur.tile, tile_first = args.step0[cur.p] + tile * p.steps;
+        const int nb = p.nb, G = 1 << p.log_g, W = kWarps >> p.log_g;
+        const int grp = warp & (G - 1), share = warp >> p.log_g;
+        const int rg = cur.rg;
+        const bool mine = rg * kRows < p.N;
         const float offset = *p.offset;
         float acc[2][NT][4] = {};
-        for (int b = warp; b < nb; b += kWarps) {
-            uint2 cw[4];
-            float am[4];
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t blk = (int64_t)(n0 + 8 * i + g) * nb + b;
-                cw[i] = __ldcs(reinterpret_cast<const uint2*>(p.packed + blk * 32 + t4 * 8));
-                // absmax = fp32(fp32(table[q] s2) + offset), the codec's own roundings
-                const int q = p.q[blk];
-                am[i] = __fadd_rn(__fmul_rn(__fdiv_rn((float)(q < 255 ? q - 127 : 0), 127.f), p.s2[blk >> 8]), offset);
+        if (p.u != nullptr && mine)             // read at the tile's end
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.B + (int64_t)(rg * kRows + lane) * args.r));
+        const char* const xf = reinterpret_cast<const char*>(p.xf) + (TP == 2 ? (g >> 1) * (TP * 128) + (g & 1) * 64 : g * 64) + t4 * 16;
+        const char* const xsp = reinterpret_cast<const char*>(p.xs) + t4 * 8;
+        for (int n = cur.here; n > 0; --n) {
+            const int ks = cur.ks;
+            cur.ks += cur.dks;
+            if (ks >= cur.stages) continue;
+            const int slot = used % kDepth;
+            const int b0 = ks * kStageBlocks;
+            const char* xb = xf + (uint32_t)(b0 * (TP * 128));
+            const char* xsb = xsp + (uint32_t)(b0 * (TP * 4));
+            uint4 xa2 = make_uint4(0, 0, 0, 0), xc2 = xa2;
+            float2 xs2 = make_float2(0.f, 0.f);
+            if constexpr (TP == 2) {            // ahead of the wait
+                if ((g & 1) < T && b0 + (g >> 1) < nb) {
+                    xa2 = *reinterpret_cast<const uint4*>(xb);
+                    xc2 = *reinterpret_cast<const uint4*>(xb + TP * 64);
+                }
+                if (b0 + t4 < nb) xs2 = *reinterpret_cast<const float2*>(xsb);
             }
-            X16 xv[NT];
-            float2 xs[NT];
-            #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                xv[i] = load16(reinterpret_cast<const uint16_t*>(p.xf) + ((int64_t)b * T + g + 8 * i) * 64 + 16 * t4, g + 8 * i < T);
-                xs[i] = *reinterpret_cast<const float2*>(p.xs + (int64_t)b * 8 * NT + 8 * i + 2 * t4);
+            if (!dead && !__all_sync(0xffffffffu, mbar_try_wait(&full[slot], (used / kDepth) & 1))) {
+                if (__any_sync(0xffffffffu, !mbar_wait(&full[slot], (used / kDepth) & 1, nullptr))) {
+                    dead = true;                // keep walking, so that the CTA's barriers stay whole
+                    if (lane == 0) atomicExch(args.err, 1);
+                }
             }
+            if (dead) continue;
+            ++used;
+            stsf4(am_sh + lane * 16, absmax4(raw[0], offset));
+            // the stage's codes, all into registers: the slot is free again before the arithmetic begins
+            const uint32_t st = ring + slot * kStageBytes;
+            uint2 cw[kStageBlocks][4];
             #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float c[NT][4] = {};
+            for (int j = 0; j < kStageBlocks; ++j)
                 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const uint32_t w0 = m < 2 ? cw[2 * h].x : cw[2 * h].y, w1 = m < 2 ? cw[2 * h + 1].x : cw[2 * h + 1].y;
-                    const int j = (2 * m) & 3;
-                    uint32_t a[4];
+                for (int i = 0; i < 4; ++i) cw[j][i] = lds64(st + (piece ^ (32 * j)) + i * 1024);
+            __syncwarp();
+            #pragma unroll
+            for (int i = 0; i + 1 < kDepth; ++i) raw[i] = raw[i + 1];
+            load_next(raw[kDepth - 1]);
+            if constexpr (TP == 2) {
+                float c[2][4] = {};
+                #pragma unroll
+                for (int j = 0; j < kStageBlocks; ++j) {
+                    const uint32_t on = (g >> 1) == j ? 0xffffffffu : 0u;
+                    const uint32_t bx[8] = {xa2.x & on, xa2.y & on, xa2.z & on, xa2.w & on, xc2.x & on, xc2.y & on, xc2.z & on, xc2.w & on};
                     #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t at = prmt((q & 1) ? w1 : w0, lane4, 0x5504u | (uint32_t)(j + (q >> 1)) << 4);
-                        a[q] = *reinterpret_cast<const uint32_t*>(smem_raw + at);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint2 u = cw[j][2 * h], v = cw[j][2 * h + 1];
+                        uint32_t a[4];
+                        operand<0>(a, u.x, v.x, lane4);
+                        mma_f16(c[h], a, bx[0], bx[1]);
+                        operand<2>(a, u.x, v.x, lane4);
+                        mma_f16(c[h], a, bx[2], bx[3]);
+                        operand<0>(a, u.y, v.y, lane4);
+                        mma_f16(c[h], a, bx[4], bx[5]);
+                        operand<2>(a, u.y, v.y, lane4);
+                        mma_f16(c[h], a, bx[6], bx[7]);
+                    }
+                }
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float lo = ldsf(am_sh + (16 * h + rowp) * 16 + t4 * 4), hi = ldsf(am_sh + (16 * h + 8 + rowp) * 16 + t4 * 4);
+                    acc[h][0][0] = fmaf(c[h][0] * xs2.x, lo, acc[h][0][0]);
+                    acc[h][0][1] = fmaf(c[h][1] * xs2.y, lo, acc[h][0][1]);
+                    acc[h][0][2] = fmaf(c[h][2] * xs2.x, hi, acc[h][0][2]);
+                    acc[h][0][3] = fmaf(c[h][3] * xs2.y, hi, acc[h][0][3]);
+                }
+            } else {
+                const int nj = min(kStageBlocks, nb - b0);
+                #pragma unroll
+                for (int j = 0; j < kStageBlocks; ++j) {
+                    if (j >= nj) break;
+                    uint4 xa[NT], xc[NT];
+                    float2 xs[NT];
+                    #pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        xa[i] = xc[i] = make_uint4(0, 0, 0, 0);
+                        if (g + 8 * i < T) {
+                            xa[i] = *reinterpret_cast<const uint4*>(xb + j * (TP * 128) + i * 512);
+                            xc[i] = *reinterpret_cast<const uint4*>(xb + j * (TP * 128) + i * 512 + TP * 64);
+                        }
+                        xs[i] = *reinterpret_cast<const float2*>(xsb + j * (TP * 4) + i * 32);
                     }
                     #pragma unroll
-                    for (int i = 0; i < NT; ++i) mma_f16(c[i], a, xv[i].w(2 * m), xv[i].w(2 * m + 1));
-                }
-                #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    acc[h][i][0] += c[i][0] * xs[i].x * am[2 * h];
-                    acc[h][i][1] += c[i][1] * xs[i].y * am[2 * h];
-                    acc[h][i][2] += c[i][2] * xs[i].x * am[2 * h + 1];
-                    acc[h][i][3] += c[i][3] * xs[i].y * am[2 * h + 1];
+                    for (int h = 0; h < 2; ++h) {
+                        const uint2 u = cw[j][2 * h], v = cw[j][2 * h + 1];
+                        const float lo = ldsf(am_sh + (16 * h + rowp) * 16 + j * 4), hi = ldsf(am_sh + (16 * h + 8 + rowp) * 16 + j * 4);
+                        float c[NT][4] = {};
+                        uint32_t a[4];
+                        operand<0>(a, u.x, v.x, lane4);
+                        #pragma unroll
+                        for (int i = 0; i < NT; ++i) mma_f16(c[i], a, xa[i].x, xa[i].y);
+                        operand<2>(a, u.x, v.x, lane4);
+                        #pragma unroll
+                        for (int i = 0; i < NT; ++i) mma_f16(c[i], a, xa[i].z, xa[i].w);
+                        operand<0>(a, u.y, v.y, lane4);
+                        #pragma unroll
+                        for (int i = 0; i < NT; ++i) mma_f16(c[i], a, xc[i].x, xc[i].y);
+                        operand<2>(a, u.y, v.y, lane4);
+                        #pragma unroll
+                        for (int i = 0; i < NT; ++i) mma_f16(c[i], a, xc[i].z, xc[i].w);
+                        #pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            acc[h][i][0] = fmaf(c[i][0] * xs[i].x, lo, acc[h][i][0]);
+                            acc[h][i][1] = fmaf(c[i][1] * xs[i].y, lo, acc[h][i][1]);
+                            acc[h][i][2] = fmaf(c[i][2] * xs[i].x, hi, acc[h][i][2]);
+                            acc[h][i][3] = fmaf(c[i][3] * xs[i].y, hi, acc[h][i][3]);
+                        }
+                    }
                 }
             }
+            __syncwarp();                       // every lane has read am_sh
         }
+        const int seg_begin = end - cur.left;
+        if (p.u != nullptr && mine && seg_begin == tile_first && share == 0) add_adapter<TP, NT>(args, p, rg * kRows + rowp, t4, acc);
+        if constexpr (TP == 2) {                // the columns of a token: the stage's blocks, one per lane of a quad
+            #pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                float& v = acc[q / 4][0][q % 4];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+            }
+        }
+
+        // the segment's sums: value q of lane (g, t4) is row
+        // 16 (q / 4 NT) + 8 (q / 2 % 2) + rowp, token 8 (q / 4 % NT) + 2 t4 + q % 2
+        float v[Q];
         #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < Q; ++q) v[q] = acc[q / (4 * NT)][(q / 4) % NT][q % 4];
+        if (W > 1) {                            // the W warps of a row group: each ends up with every W-th value
             #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                float* d = part + ((warp * kRows + 16 * h + g) * 8 * NT + 8 * i + 2 * t4);
-                *reinterpret_cast<float2*>(d) = make_float2(acc[h][i][0], acc[h][i][1]);
-                *reinterpret_cast<float2*>(d + 8 * 8 * NT) = make_float2(acc[h][i][2], acc[h][i][3]);
-            }
-        __syncthreads();
-        for (int o = threadIdx.x; o < kRows * T; o += kThreads) {
-            const int t = o / kRows, row = o % kRows;
-            float s = 0.f;
+            for (int q = 0; q < Q; ++q) stsf((warp * Q + q) * 256 + 128 + lane4, v[q]);
+            __syncthreads();
             #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += part[(w * kRows + row) * 8 * NT + t];
-            if (p.u != nullptr) {
-                const uint4* B = reinterpret_cast<const uint4*>(p.B + (int64_t)(n0 + row) * r);
-                const float* u = p.u + (int64_t)t * r;
-                float d = 0.f;
-                for (int j = 0; j < r; j += 8) {
-                    const uint4 v = B[j / 8];
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        d = fmaf(u[j + 2 * q], bf16_f(w[q] & 0xffffu), d);
-                        d = fmaf(u[j + 2 * q + 1], __uint_as_float(w[q] & 0xffff0000u), d);
-                    }
-                }
-                s = fmaf(args.scale, d, s);
+            for (int q = 0; q < Q; ++q) {
+                if (q % W != share) continue;
+                float s = 0.f;
+                for (int w = 0; w < W; ++w) s += ldsf(((grp + w * G) * Q + q) * 256 + 128 + lane4);
+                v[q] = s;
             }
-            p.y[(int64_t)t * p.N + n0 + row] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+            __syncthreads();
         }
-        __syncthreads();
+        const int first = cta_of(args, tile_first), last = cta_of(args, tile_first + p.steps - 1);
+        bool write = mine;
+        if (first != last && mine && share < Q) {
+            float* const part = args.part;
+            const int slot = 2 * blockIdx.x + (seg_begin == begin ? 0 : 1);
+            #pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if (q % W == share) __stcg(&part[((int64_t)(slot * kWarps + grp) * Q + q) * 32 + lane], v[q]);
+            __syncwarp();
+            int done = 0;
+            int* const counter = args.counters + p.counter0 + rg * W + share;
+            if (lane == 0) asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
+            done = __shfl_sync(0xffffffffu, done, 0);
+            __syncwarp();
+            write = done == last - first;
+            if (write) {
+                #pragma unroll
+                for (int q = 0; q < Q; ++q) v[q] = 0.f;
+                #pragma unroll 4
+                for (int c = first; c <= last; ++c) {
+                    const int at = 2 * c + (c > first || first_step(args, c) == tile_first ? 0 : 1);
+                    #pragma unroll
+                    for (int q = 0; q < Q; ++q)
+                        if (q % W == share) v[q] += __ldcg(&part[((int64_t)(at * kWarps + grp) * Q + q) * 32 + lane]);
+                }
+            }
+        }
+        if (write && !dead) {
+            #pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (q % W != share) continue;
+                const int row = rg * kRows + 16 * (q / (4 * NT)) + 8 * ((q / 2) & 1) + rowp, t = 8 * ((q / 4) % NT) + 2 * t4 + (q & 1);
+                if (t < T && (TP > 2 || t4 == 0)) p.y[(int64_t)t * p.N + row] = __bfloat16_as_ushort(__float2bfloat16_rn(v[q]));
+            }
+        }
+        cur.left -= cur.here;
+        if (cur.left > 0) cur.next_tile(args, warp);
     }
+    if (dead)                                   // copies still on their way must land before the CTA ends
+        for (; used < issued; ++used) mbar_wait(&full[used % kDepth], (used / kDepth) & 1, nullptr);
 }
 
-template <int NT>
-lsn_status launch_nt(const PrepArgs& pa, const DecodeArgs& da, cudaStream_t st) {
+template <int TP>
+lsn_status launch_tp(const PrepArgs& pa, const DecodeArgs& da, int grid, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};      // devices that know the kernel's shared memory size
+    int dev = 0;
+    LSN_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev >= 64 || !(ready.load() >> dev & 1)) {
+        LSN_CUDA_TRY(cudaFuncSetAttribute(lsn_decode_kernel<TP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+        if (dev < 64) ready.fetch_or(1ull << dev);
+    }
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kPrepCtas, (unsigned)((pa.r + 15) / 16), (unsigned)da.n);
@@ -317,44 +735,66 @@ lsn_status launch_nt(const PrepArgs& pa, const DecodeArgs& da, cudaStream_t st) 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1 + pdl_attr(&at[1]);
-    LSN_CUDA_TRY(cudaLaunchKernelEx(&cfg, lsn_decode_prep_kernel<NT>, pa));
-    const int smem = kTableBytes + kWarps * kRows * 8 * NT * 4;
-    LSN_CUDA_TRY(cudaFuncSetAttribute(lsn_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    LSN_CUDA_TRY(cudaLaunchKernelEx(&cfg, lsn_decode_prep_kernel<TP>, pa));
     cfg = cudaLaunchConfig_t{};
-    cfg.gridDim = dim3((unsigned)std::min(da.tiles, sm_count()));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = pdl_attr(&at[0]);
-    LSN_CUDA_TRY(cudaLaunchKernelEx(&cfg, lsn_decode_kernel<NT>, da));
+    LSN_CUDA_TRY(cudaLaunchKernelEx(&cfg, lsn_decode_kernel<TP>, da));
     return LSN_OK;
 }
 
-}  // namespace
+// How a projection is cut into steps (T tokens): the warps of a CTA share out
+// G row groups and W = 16 / G stages along K.
+struct Cut {
+    int log_g, steps, tiles;
+};
+Cut cut_of(int64_t N, int64_t K, int64_t per_cta) {
+    const int64_t stages = ceil_div(K / 64, kStageBlocks), groups = N / kRows;
+    int lg = per_cta < 2 ? 0 : 4;
+    while (lg < 4 && (kWarps >> lg) > stages) ++lg;
+    Cut c;
+    c.log_g = lg;
+    c.steps = (int)ceil_div(stages, kWarps >> lg);
+    c.tiles = (int)ceil_div(groups, 1 << lg);
+    return c;
+}
 
-// Workspace: 256 bytes reserved, then per projection u, the fp16 x and its block scales.
-namespace {
+// Workspace: the status word (256 bytes), then the counters, the partial sums
+// and per projection u, the fp16 x and its block scales.
 struct DecodeWs {
+    int* err;
+    int* counters;
+    float* part;
     float* u[LSN_LAYER_MAX_PROJ];
     __half* xf[LSN_LAYER_MAX_PROJ];
     float* xs[LSN_LAYER_MAX_PROJ];
     size_t total;
 };
+int pad_tokens(int64_t T) { return T <= 2 ? 2 : T <= 8 ? 8 : 16; }
 DecodeWs carve_decode(void* ws, int n, const lsn_lora_proj* p, int64_t T, int r) {
     DecodeWs w{};
-    size_t off = 256;
+    size_t off = 0;
     char* b = reinterpret_cast<char*>(ws);
     auto take = [&](size_t bytes) { char* q = b ? b + off : nullptr; off += round_up(bytes, 256); return q; };
+    w.err = reinterpret_cast<int*>(take(256));
+    size_t counters = 0;
+    for (int i = 0; i < n; ++i) counters += (size_t)(p[i].W.rows / kRows + kWarps) * kWarps;
+    w.counters = reinterpret_cast<int*>(take(counters * 4));
+    w.part = reinterpret_cast<float*>(take((size_t)kMaxGrid * 2 * kWarps * kRows * LSN_DECODE_MAX_T * 4));
     for (int i = 0; i < n; ++i) {
         const size_t K = (size_t)p[i].W.cols;
         w.u[i] = reinterpret_cast<float*>(take((size_t)T * r * 4));
-        w.xf[i] = reinterpret_cast<__half*>(take((size_t)T * K * 2));
+        w.xf[i] = reinterpret_cast<__half*>(take((size_t)pad_tokens(T) * K * 2));
         w.xs[i] = reinterpret_cast<float*>(take(K / 64 * LSN_DECODE_MAX_T * 4));
     }
     w.total = off;
     return w;
 }
+
 }  // namespace
 
 size_t decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r) { return carve_decode(nullptr, n, p, T, r).total; }
@@ -362,27 +802,44 @@ size_t decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r) { return
 lsn_status launch_decode(int n, const lsn_lora_proj* p, int T, int r, float scale, void* ws, cudaStream_t st) {
     const DecodeWs w = carve_decode(ws, n, p, T, r);
     PrepArgs pa{};
-    DecodeArgs da{};
+    DecodeArgs da;
     pa.T = da.T = T;
     pa.r = da.r = r;
     da.n = n;
     da.scale = scale;
+    da.err = w.err;
+    da.part = w.part;
+    pa.counters = da.counters = w.counters;
     std::copy(nf4_tables().level, nf4_tables().level + 16, da.level);
-    int64_t tiles = 0;
+    int64_t total = 0, counters = 0, work = 0;
+    std::fill(da.step0, da.step0 + LSN_LAYER_MAX_PROJ, INT32_MAX);
+    for (int i = 0; i < n; ++i) work += p[i].W.rows / kRows * ceil_div(p[i].W.cols / 64, kStageBlocks);
+    const int64_t per_cta = work / (kWarps * kMaxGrid);
     for (int i = 0; i < n; ++i) {
         const lsn_lora_proj& q = p[i];
         int lead = 0;                       // the first projection that reads the same x
         while (p[lead].x != q.x || p[lead].W.cols != q.W.cols) ++lead;
         const bool off = q.A == nullptr;
-        pa.p[i] = PrepProj{q.x, q.A, w.u[i], lead == i ? w.xf[i] : nullptr, w.xs[i], (int)(q.W.cols / 64)};
+        const int nb = (int)(q.W.cols / 64);
+        pa.p[i] = PrepProj{q.x, q.A, w.u[i], lead == i ? w.xf[i] : nullptr, w.xs[i], nb};
         const lsn_nf4_weight& f = q.W.nf4;
-        da.p[i] = DecodeProj{f.packed, f.absmax_q, f.absmax_s2, f.offset, w.xf[lead], w.xs[lead], off ? nullptr : w.u[i], q.B, q.y,
-                             (int)(q.W.cols / 64), (int)q.W.rows, (int)tiles};
-        tiles += q.W.rows / kRows;
-        if (tiles > INT32_MAX) return fail(LSN_ERR_UNSUPPORTED, "lora_layer_decode: too many rows");
+        const Cut c = cut_of(q.W.rows, q.W.cols, per_cta);
+        const uintptr_t qa = reinterpret_cast<uintptr_t>(f.absmax_q) | (uintptr_t)nb;
+        da.p[i] = DecodeProj{f.absmax_q, f.absmax_s2, f.offset, w.xf[lead], w.xs[lead], off ? nullptr : w.u[i], q.B, q.y, nb, (int)q.W.rows,
+                             c.log_g, c.steps, c.tiles, (int)ceil_div(nb, kStageBlocks), (int)counters, qa % 4 == 0 ? 4 : qa % 2 == 0 ? 2 : 1};
+        da.step0[i] = (int)total;
+        // the packed codes as 16-bit elements: rows of K / 4, boxes of 64 x 32
+        lsn_status s = make_tmap_2d(&da.map[i], f.packed, q.W.cols / 4, q.W.rows, q.W.cols / 4, 64, kRows, false);
+        if (s != LSN_OK) return s;
+        total += (int64_t)c.steps * c.tiles;
+        counters += (int64_t)c.tiles * kWarps;
+        if (total > INT32_MAX / 2 || q.W.rows * nb > (int64_t)UINT32_MAX) return fail(LSN_ERR_UNSUPPORTED, "lora_layer_decode: weights too large");
     }
-    da.tiles = (int)tiles;
-    return T <= 8 ? launch_nt<1>(pa, da, st) : launch_nt<2>(pa, da, st);
+    const int grid = (int)std::min<int64_t>({total, sm_count(), kMaxGrid});
+    da.per = (int)(total / grid);
+    da.rem = (int)(total % grid);
+    pa.n_counters = (int)counters;
+    return T <= 2 ? launch_tp<2>(pa, da, grid, st) : T <= 8 ? launch_tp<8>(pa, da, grid, st) : launch_tp<16>(pa, da, grid, st);
 }
 
 }  // namespace lsn

@@ -79,7 +79,9 @@ def _ws(lib, projs, T, r, fill=0xFF):
     import torch
     n = lib.decode_ws_bytes(projs, T, r)
     assert n > 0
-    return torch.full((n,), fill, dtype=torch.uint8, device="cuda"), n
+    ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0                                       # the status word; the rest needs no value
+    return ws, n
 
 
 def run_single(lib, p, ws=None, stream=None):
