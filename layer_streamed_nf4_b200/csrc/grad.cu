@@ -13,18 +13,20 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTensors = 1024;          // of one launch (28 bytes of kernel parameters each)
+constexpr int kFewTensors = 16;            // launches of up to so many take a small parameter block
 constexpr int kChunkBytes = 16384;         // one CTA's piece of a tensor at a time
 constexpr int kMaxCtas = 2048;             // partial sums per launch
 
 // Tensors of one launch; tensor i covers chunks chunk0[i] .. chunk0[i + 1].
+template <int MAX>
 struct GradArgs {
-    const void* src[kMaxTensors];
-    void* dst[kMaxTensors];
-    uint64_t numel[kMaxTensors];           // bit 63: bf16
-    int chunk0[kMaxTensors];
     int n, chunks;
+    int chunk0[MAX];
+    const void* src[MAX];
+    void* dst[MAX];
+    uint64_t numel[MAX];                   // bit 63: bf16
 };
-static_assert(sizeof(GradArgs) + 64 <= 32764, "kernel parameters");
+static_assert(sizeof(GradArgs<kMaxTensors>) + 64 <= 32764, "kernel parameters");
 
 // Head of the workspace: the scale for the clip kernel, the count of finished
 // CTAs (zero between calls), then one fp64 partial sum per CTA and launch.
@@ -35,7 +37,8 @@ struct GradWs {
 };
 constexpr size_t kWsHead = 256;
 
-__device__ __forceinline__ int tensor_of(const GradArgs& a, int chunk) {
+template <int MAX>
+__device__ __forceinline__ int tensor_of(const GradArgs<MAX>& a, int chunk) {
     int lo = 0, hi = a.n - 1;              // the last tensor whose first chunk is <= chunk
     while (lo < hi) {
         const int m = (lo + hi + 1) >> 1;
@@ -51,7 +54,8 @@ struct Chunk {
     int lo, hi;            // its elements' bounds within the tensor, in elements from base
     bool bf16;
 };
-__device__ __forceinline__ Chunk chunk_of(const GradArgs& a, int i, int chunk) {
+template <int MAX>
+__device__ __forceinline__ Chunk chunk_of(const GradArgs<MAX>& a, int i, int chunk) {
     const uint64_t nm = a.numel[i];
     Chunk c;
     c.bf16 = nm >> 63;
@@ -78,6 +82,26 @@ __device__ __forceinline__ double squares4(float a, float b, float c, float d) {
     return (double)a * a + (double)b * b + (double)c * c + (double)d * d;
 }
 
+__device__ __forceinline__ double squares_of(const uint4& v, bool bf16) {
+    if (bf16)
+        return squares4(lo_bf16(v.x), hi_bf16(v.x), lo_bf16(v.y), hi_bf16(v.y)) + squares4(lo_bf16(v.z), hi_bf16(v.z), lo_bf16(v.w), hi_bf16(v.w));
+    return squares4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ uint4 scaled(uint4 v, float f, bool bf16) {
+    if (bf16) {
+        v.x = pack_bf16x2(lo_bf16(v.x) * f, hi_bf16(v.x) * f);
+        v.y = pack_bf16x2(lo_bf16(v.y) * f, hi_bf16(v.y) * f);
+        v.z = pack_bf16x2(lo_bf16(v.z) * f, hi_bf16(v.z) * f);
+        v.w = pack_bf16x2(lo_bf16(v.w) * f, hi_bf16(v.w) * f);
+    } else {
+        v.x = __float_as_uint(__uint_as_float(v.x) * f);
+        v.y = __float_as_uint(__uint_as_float(v.y) * f);
+        v.z = __float_as_uint(__uint_as_float(v.z) * f);
+        v.w = __float_as_uint(__uint_as_float(v.w) * f);
+    }
+    return v;
+}
+
 __device__ double block_sum(double v, double* sh) {
     #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -94,24 +118,29 @@ __device__ double block_sum(double v, double* sh) {
 
 // Partial sums of one launch's tensors; with `last`, the last CTA to finish
 // adds those of every launch (`parts` in all, in order) and writes the norm.
-__global__ void __launch_bounds__(kThreads) lsn_grad_norm_kernel(const __grid_constant__ GradArgs a, GradWs* ws, int part0, int parts, bool last,
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) lsn_grad_norm_kernel(const __grid_constant__ GradArgs<MAX> a, GradWs* ws, int part0, int parts, bool last,
                                                                  float max_norm, float* norm) {
     __shared__ double sh[kThreads / 32];
     __shared__ int is_last;
     pdl_wait();
+    pdl_launch_dependents();
     double sum = 0.0;
     for (int ch = blockIdx.x; ch < a.chunks; ch += gridDim.x) {
         const Chunk c = chunk_of(a, tensor_of(a, ch), ch);
         const int per = c.bf16 ? 8 : 4;
+        if (c.lo == 0 && c.hi == kChunkBytes / (c.bf16 ? 2 : 4)) {      // a whole chunk: four words of a thread at once
+            uint4 v[kChunkBytes / 16 / kThreads];
+            #pragma unroll
+            for (int u = 0; u < kChunkBytes / 16 / kThreads; ++u) v[u] = reinterpret_cast<const uint4*>(c.base)[threadIdx.x + u * kThreads];
+            #pragma unroll
+            for (int u = 0; u < kChunkBytes / 16 / kThreads; ++u) sum += squares_of(v[u], c.bf16);
+            continue;
+        }
         for (int w = threadIdx.x; w * per < c.hi; w += kThreads) {
             const int e = w * per;
             if (e >= c.lo && e + per <= c.hi) {
-                const uint4 v = *reinterpret_cast<const uint4*>(c.base + 16 * w);
-                if (c.bf16)
-                    sum += squares4(lo_bf16(v.x), hi_bf16(v.x), lo_bf16(v.y), hi_bf16(v.y)) +
-                           squares4(lo_bf16(v.z), hi_bf16(v.z), lo_bf16(v.w), hi_bf16(v.w));
-                else
-                    sum += squares4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+                sum += squares_of(*reinterpret_cast<const uint4*>(c.base + 16 * w), c.bf16);
             } else {
                 for (int k = max(e, c.lo); k < min(e + per, c.hi); ++k) {
                     const double g = c.bf16 ? (double)lo_bf16(reinterpret_cast<const uint16_t*>(c.base)[k])
@@ -145,10 +174,13 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_norm_kernel(const __grid_co
     }
 }
 
-__global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_constant__ GradArgs a, const GradWs* ws) {
+// The last chunks first: they are what the norm read last and the L2 still holds.
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_constant__ GradArgs<MAX> a, const GradWs* ws) {
     pdl_wait();
+    pdl_launch_dependents();
     const float f = ws->factor;
-    for (int ch = blockIdx.x; ch < a.chunks; ch += gridDim.x) {
+    for (int ch = a.chunks - 1 - (int)blockIdx.x; ch >= 0; ch -= (int)gridDim.x) {
         const int i = tensor_of(a, ch);
         const Chunk c = chunk_of(a, i, ch);
         char* const dst = reinterpret_cast<char*>(a.dst[i]) + (c.base - reinterpret_cast<const char*>(a.src[i]));
@@ -156,22 +188,19 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_c
         const int es = c.bf16 ? 2 : 4;
         const int per = 16 / es;
         const bool wide = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+        if (wide && c.lo == 0 && c.hi == kChunkBytes / es) {            // a whole chunk: four words of a thread at once
+            uint4 v[kChunkBytes / 16 / kThreads];
+            #pragma unroll
+            for (int u = 0; u < kChunkBytes / 16 / kThreads; ++u) v[u] = reinterpret_cast<const uint4*>(c.base)[threadIdx.x + u * kThreads];
+            #pragma unroll
+            for (int u = 0; u < kChunkBytes / 16 / kThreads; ++u) __stcs(reinterpret_cast<uint4*>(dst) + threadIdx.x + u * kThreads, scaled(v[u], f, c.bf16));
+            continue;
+        }
         for (int w = threadIdx.x; w * per < c.hi; w += kThreads) {
             const int e = w * per;
             if (wide && e >= c.lo && e + per <= c.hi) {
-                uint4 v = *reinterpret_cast<const uint4*>(c.base + 16 * w);
-                if (c.bf16) {
-                    v.x = pack_bf16x2(lo_bf16(v.x) * f, hi_bf16(v.x) * f);
-                    v.y = pack_bf16x2(lo_bf16(v.y) * f, hi_bf16(v.y) * f);
-                    v.z = pack_bf16x2(lo_bf16(v.z) * f, hi_bf16(v.z) * f);
-                    v.w = pack_bf16x2(lo_bf16(v.w) * f, hi_bf16(v.w) * f);
-                } else {
-                    v.x = __float_as_uint(__uint_as_float(v.x) * f);
-                    v.y = __float_as_uint(__uint_as_float(v.y) * f);
-                    v.z = __float_as_uint(__uint_as_float(v.z) * f);
-                    v.w = __float_as_uint(__uint_as_float(v.w) * f);
-                }
-                *reinterpret_cast<uint4*>(dst + 16 * w) = v;
+                const uint4 v = *reinterpret_cast<const uint4*>(c.base + 16 * w);
+                __stcs(reinterpret_cast<uint4*>(dst + 16 * w), scaled(v, f, c.bf16));
             } else {
                 for (int k = max(e, c.lo); k < min(e + per, c.hi); ++k) {
                     if (c.bf16)
@@ -189,6 +218,31 @@ int64_t chunks_of(const lsn_grad& t) {
     const int es = t.dtype == LSN_DT_BF16 ? 2 : 4;
     const int64_t mis = (int64_t)(reinterpret_cast<uintptr_t>(t.src) & 15) / es;
     return t.numel == 0 ? 0 : ceil_div(t.numel + mis, kChunkBytes / es);
+}
+
+// The next tensors of t[*i ..], up to kMaxTensors, as one launch's arguments;
+// those that go on where the one before ends (the tensors of one flat buffer)
+// count as one.  *i becomes the first tensor left over.
+void fill(GradArgs<kMaxTensors>& a, const lsn_grad* t, int n, int* i, bool clip) {
+    a.n = a.chunks = 0;
+    for (; *i < n; ++*i) {
+        lsn_grad r = t[*i];
+        if (r.numel == 0) continue;
+        if (a.n == kMaxTensors) return;
+        const int64_t es = r.dtype == LSN_DT_BF16 ? 2 : 4;
+        for (; *i + 1 < n; ++*i) {
+            const lsn_grad& q = t[*i + 1];
+            if (q.numel != 0 && (q.dtype != r.dtype || q.src != reinterpret_cast<const char*>(r.src) + es * r.numel ||
+                                 (clip && q.dst != reinterpret_cast<char*>(r.dst) + es * r.numel)))
+                break;
+            r.numel += q.numel;
+        }
+        a.src[a.n] = r.src;
+        a.dst[a.n] = r.dst;
+        a.numel[a.n] = (uint64_t)r.numel | (r.dtype == LSN_DT_BF16 ? 1ull << 63 : 0);
+        a.chunk0[a.n++] = a.chunks;
+        a.chunks += (int)chunks_of(r);
+    }
 }
 
 template <class... P, class... A>
@@ -217,17 +271,17 @@ lsn_status grad_call(int n, const lsn_grad* t, bool clip, float max_norm, float*
     LSN_CHECK_ARG(ws_bytes >= ws_bytes_of(n), f + ": workspace too small (need " + std::to_string(ws_bytes_of(n)) + " bytes)");
     int64_t chunks = 0;
     double bytes = 0.0;
+    auto fi = [&](int i, const char* what) { return f + ": tensor " + std::to_string(i) + what; };
     for (int i = 0; i < n; ++i) {
-        const std::string fi = f + ": tensor " + std::to_string(i);
-        LSN_CHECK_ARG(t[i].numel >= 0 && t[i].numel <= (int64_t)1 << 42, fi + ": numel out of range");
-        LSN_CHECK_ARG(t[i].dtype == LSN_DT_BF16 || t[i].dtype == LSN_DT_F32, fi + ": unknown type");
+        LSN_CHECK_ARG(t[i].numel >= 0 && t[i].numel <= (int64_t)1 << 42, fi(i, ": numel out of range"));
+        LSN_CHECK_ARG(t[i].dtype == LSN_DT_BF16 || t[i].dtype == LSN_DT_F32, fi(i, ": unknown type"));
         const uintptr_t es = t[i].dtype == LSN_DT_BF16 ? 2 : 4;
         if (t[i].numel == 0) continue;
-        LSN_CHECK_ARG(t[i].src != nullptr && (reinterpret_cast<uintptr_t>(t[i].src) % es) == 0, fi + ": src must be aligned to its type");
+        LSN_CHECK_ARG(t[i].src != nullptr && (reinterpret_cast<uintptr_t>(t[i].src) % es) == 0, fi(i, ": src must be aligned to its type"));
         if (clip) {
-            LSN_CHECK_ARG(t[i].dst != nullptr && (reinterpret_cast<uintptr_t>(t[i].dst) % es) == 0, fi + ": dst must be aligned to its type");
+            LSN_CHECK_ARG(t[i].dst != nullptr && (reinterpret_cast<uintptr_t>(t[i].dst) % es) == 0, fi(i, ": dst must be aligned to its type"));
             const uintptr_t a = reinterpret_cast<uintptr_t>(t[i].src), b = reinterpret_cast<uintptr_t>(t[i].dst), k = es * (uintptr_t)t[i].numel;
-            LSN_CHECK_ARG(a == b || a + k <= b || b + k <= a, fi + ": dst overlaps src in part");
+            LSN_CHECK_ARG(a == b || a + k <= b || b + k <= a, fi(i, ": dst overlaps src in part"));
         }
         chunks += chunks_of(t[i]);
         bytes += (double)es * (double)t[i].numel * (clip ? 2.0 : 1.0);
@@ -236,34 +290,40 @@ lsn_status grad_call(int n, const lsn_grad* t, bool clip, float max_norm, float*
     lsn_status s = check_device();
     if (s != LSN_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int batches = (int)std::max<int64_t>(1, ceil_div(n, kMaxTensors));
-    TimingScope ts(LSN_K_GRAD, bytes, st, clip ? 2 * batches : batches);
-    GradArgs a;
-    auto fill = [&](int b) {
-        a.n = std::max(1, std::min(n - b * kMaxTensors, kMaxTensors));
-        a.chunks = 0;
-        for (int i = 0; i < a.n; ++i) {
-            const lsn_grad none{};
-            const lsn_grad& q = n == 0 ? none : t[b * kMaxTensors + i];
-            a.src[i] = q.src;
-            a.dst[i] = q.dst;
-            a.numel[i] = (uint64_t)q.numel | (q.dtype == LSN_DT_BF16 ? 1ull << 63 : 0);
-            a.chunk0[i] = a.chunks;
-            a.chunks += (int)chunks_of(q);
-        }
-        return std::max(1, std::min({a.chunks, 8 * sm_count(), kMaxCtas}));
+    TimingScope ts(LSN_K_GRAD, bytes, st, clip ? 2 : 1);
+    GradArgs<kMaxTensors> a;
+    GradArgs<kFewTensors> few;
+    auto grid_of = [&] { return std::max(1, std::min({a.chunks, 8 * sm_count(), kMaxCtas})); };
+    auto is_few = [&] {                     // a small copy of the arguments, when they fit one
+        if (a.n > kFewTensors) return false;
+        few.n = a.n;
+        few.chunks = a.chunks;
+        std::copy(a.chunk0, a.chunk0 + a.n, few.chunk0);
+        std::copy(a.src, a.src + a.n, few.src);
+        std::copy(a.dst, a.dst + a.n, few.dst);
+        std::copy(a.numel, a.numel + a.n, few.numel);
+        return true;
     };
-    int parts = 0;
-    for (int b = 0; b < batches; ++b) {
-        const int grid = fill(b);
-        s = launch(lsn_grad_norm_kernel, grid, st, a, (GradWs*)ws, parts, parts + grid, b + 1 == batches, max_norm, norm);
+    int parts = 0, i = 0, launches = 0;
+    do {
+        fill(a, t, n, &i, clip);
+        const int grid = grid_of();
+        s = is_few() ? launch(lsn_grad_norm_kernel<kFewTensors>, grid, st, few, (GradWs*)ws, parts, parts + grid, i >= n, max_norm, norm)
+                     : launch(lsn_grad_norm_kernel<kMaxTensors>, grid, st, a, (GradWs*)ws, parts, parts + grid, i >= n, max_norm, norm);
         if (s != LSN_OK) return s;
         parts += grid;
-    }
-    for (int b = 0; b < batches && clip; ++b) {
-        const int grid = batches == 1 ? std::max(1, std::min({a.chunks, 8 * sm_count(), kMaxCtas})) : fill(b);
-        if ((s = launch(lsn_grad_scale_kernel, grid, st, a, (const GradWs*)ws)) != LSN_OK) return s;
-    }
+        ++launches;
+    } while (i < n);
+    if (!clip) return LSN_OK;
+    i = 0;
+    do {
+        if (launches > 1) fill(a, t, n, &i, clip);
+        else i = n;
+        const int grid = grid_of();
+        s = is_few() ? launch(lsn_grad_scale_kernel<kFewTensors>, grid, st, few, (const GradWs*)ws)
+                     : launch(lsn_grad_scale_kernel<kMaxTensors>, grid, st, a, (const GradWs*)ws);
+        if (s != LSN_OK) return s;
+    } while (i < n);
     return LSN_OK;
 }
 

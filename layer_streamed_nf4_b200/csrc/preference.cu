@@ -15,13 +15,33 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMinSplit = 4096;            // logits of a row that one CTA takes at least
-constexpr int kItems = 148 * 8;            // work items wanted: below as many rows, rows are split
+constexpr int kItems = 148 * 8 * 4;        // work items wanted: below as many rows, rows are split
+constexpr int kFinThreads = 512;           // of the finishing kernel: half of them for each sequence of a pair
 constexpr size_t kWsHead = 256;
 
 // Pieces a row is cut into, from the shape alone.
 int row_splits(int64_t T, int64_t V) {
     if (T <= 0) return 1;
     return (int)std::max<int64_t>(1, std::min(ceil_div(kItems, T), V / kMinSplit));
+}
+
+// The workspace behind its head: a row's pieces, its target's logit, its gradient's factor.
+struct Scratch {
+    float2* part;                          // [T, splits] maximum and sum
+    float* ly;                             // [T]
+    float* coef;                           // [T]
+    size_t total;
+};
+Scratch carve(void* ws, int64_t T, int64_t V) {
+    Scratch w;
+    char* b = reinterpret_cast<char*>(ws);
+    size_t off = kWsHead;
+    auto take = [&](size_t bytes) { char* q = b ? b + off : nullptr; off += round_up(bytes, 256); return q; };
+    w.part = reinterpret_cast<float2*>(take((size_t)T * row_splits(T, V) * sizeof(float2)));
+    w.ly = reinterpret_cast<float*>(take((size_t)T * 4));
+    w.coef = reinterpret_cast<float*>(take((size_t)T * 4));
+    w.total = off;
+    return w;
 }
 
 struct Ws {
@@ -86,92 +106,93 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
     m = top;
 }
 
-// First and last full 16-byte word of piece `split` of a row, in words from
-// the row's start rounded down to 16 bytes.
+// The 16-byte words of a row that can be taken whole, counted from `row`
+// rounded down to 16 bytes (word w holds elements w per - mis ..): all full
+// ones, less `skip` at either end; the rest of the row is its edge, less than
+// 4 words.  Piece `split` takes words w0 .. w1.
 struct Piece {
-    int w0, w1, mis;
+    int w0, w1, mis, head, tail;           // edge: elements below head and from tail on
 };
 template <class E>
-__device__ __forceinline__ Piece piece_of(const void* row, int V, int split, int splits) {
+__device__ __forceinline__ Piece piece_of(const void* row, int V, int split, int splits, int skip) {
     constexpr int per = Words<E>::per;
     Piece p;
     p.mis = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(E);
-    const int first = p.mis ? 1 : 0, end = (V + p.mis) / per;
-    const int64_t n = end > first ? end - first : 0;
-    p.w0 = first + (int)(n * split / splits);
-    p.w1 = first + (int)(n * (split + 1) / splits);
+    const int first = (p.mis ? 1 : 0) + skip, end = (V + p.mis) / per - skip;
+    const int n = max(end - first, 0);
+    p.w0 = first + (int)((int64_t)n * split / splits);
+    p.w1 = first + (int)((int64_t)n * (split + 1) / splits);
+    p.head = n > 0 ? first * per - p.mis : V;
+    p.tail = n > 0 ? end * per - p.mis : V;
     return p;
 }
-// Element i (< 2 per) of a row that lies in no full word, or -1.
-template <class E>
-__device__ __forceinline__ int edge_of(int V, int mis, int i) {
-    constexpr int per = Words<E>::per;
-    const int head = mis ? min(per - mis, V) : 0;
-    if (i < head) return i;
-    const int end = max((V + mis) / per * per - mis, head), e = end + i - head;
-    return e < V ? e : -1;
-}
 
-// (m, s) of one piece of one row per work item.  Bound by reading the logits.
+// (m, s) of one piece of one row per CTA, and the target's logit.  Bound by
+// reading the logits; each thread keeps four 16-byte loads in flight, and the
+// special-function unit (one exp2 a logit) is busy for about two thirds of
+// the time that takes.  CTAs are handed out as others finish: rows that are
+// not scored cost nothing.
 template <class E>
-__global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_constant__ Rows r, float2* part) {
+__global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_constant__ Rows r, float2* part, float* ly) {
     constexpr int per = Words<E>::per;
     constexpr int U = 4;
     __shared__ float2 sh[kThreads / 32];
     pdl_wait();
-    const int64_t items = (int64_t)r.T * r.splits;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int t = (int)(it / r.splits), split = (int)(it % r.splits);
-        if (!scored(r, t, r.targets[t])) continue;
-        const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
-        const Piece p = piece_of<E>(row, r.V, split, r.splits);
-        const uint4* words = reinterpret_cast<const uint4*>(row - p.mis);
-        float m = -INFINITY, s = 0.f;
-        for (int w = p.w0 + threadIdx.x; w < p.w1; w += U * kThreads) {
-            float v[U][per];
-            #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (w + u * kThreads < p.w1) {
-                    Words<E>::get(words[w + u * kThreads], v[u]);
-                } else {
-                    #pragma unroll
-                    for (int i = 0; i < per; ++i) v[u][i] = -INFINITY;
-                }
-            }
-            float top = m;
-            #pragma unroll
-            for (int u = 0; u < U; ++u)
-                #pragma unroll
-                for (int i = 0; i < per; ++i) top = fmaxf(top, v[u][i]);
-            const float at = top == -INFINITY ? 0.f : top;
-            s *= ex2((m - at) * kLog2e);
-            m = top;
-            #pragma unroll
-            for (int u = 0; u < U; ++u)
-                #pragma unroll
-                for (int i = 0; i < per; ++i) s += ex2((v[u][i] - at) * kLog2e);
-        }
-        if (split == 0 && threadIdx.x < 2 * per) {
-            const int e = edge_of<E>(r.V, p.mis, threadIdx.x);
-            if (e >= 0) {
-                const float x = Words<E>::one(row + e);
-                join(m, s, x, x == -INFINITY ? 0.f : x - x + 1.f);     // NaN and +infinity give NaN
-            }
-        }
+    pdl_launch_dependents();
+    const int t = (int)(blockIdx.x / (unsigned)r.splits), split = (int)(blockIdx.x % (unsigned)r.splits);
+    const int y = r.targets[t];
+    if (!scored(r, t, y)) return;
+    const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
+    const Piece p = piece_of<E>(row, r.V, split, r.splits, 0);
+    const uint4* words = reinterpret_cast<const uint4*>(row - p.mis);
+    float m = -INFINITY, s = 0.f;
+    for (int w = p.w0 + threadIdx.x; w < p.w1; w += U * kThreads) {
+        float v[U][per];
         #pragma unroll
-        for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(m, s);
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kThreads / 32; ++w) join(m, s, sh[w].x, sh[w].y);
-            part[it] = make_float2(m, s);
+        for (int u = 0; u < U; ++u) {
+            if (w + u * kThreads < p.w1) {
+                Words<E>::get(words[w + u * kThreads], v[u]);
+            } else {
+                #pragma unroll
+                for (int i = 0; i < per; ++i) v[u][i] = -INFINITY;
+            }
         }
-        __syncthreads();
+        float top = m;
+        #pragma unroll
+        for (int u = 0; u < U; ++u)
+            #pragma unroll
+            for (int i = 0; i < per; ++i) top = fmaxf(top, v[u][i]);
+        const float at = top == -INFINITY ? 0.f : top;
+        s *= ex2((m - at) * kLog2e);
+        m = top;
+        #pragma unroll
+        for (int u = 0; u < U; ++u)
+            #pragma unroll
+            for (int i = 0; i < per; ++i) s += ex2((v[u][i] - at) * kLog2e);
+    }
+    if (split == 0) {
+        if (threadIdx.x == 0) ly[t] = Words<E>::one(row + y);
+        const int edge = p.head + r.V - p.tail;
+        if ((int)threadIdx.x < edge) {
+            const int e = (int)threadIdx.x < p.head ? (int)threadIdx.x : p.tail + (int)threadIdx.x - p.head;
+            const float x = Words<E>::one(row + e);
+            join(m, s, x, x == -INFINITY ? 0.f : x - x + 1.f);     // NaN and +infinity give NaN
+        }
+    }
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 32; ++w) join(m, s, sh[w].x, sh[w].y);
+        part[blockIdx.x] = make_float2(m, s);
     }
 }
 
 struct Finish {
     const float2* part;
+    const float* ly;
+    float* coef;                           // NULL: no gradient follows in this call
     float* lse;
     double* logp;
     int32_t* count;
@@ -185,18 +206,6 @@ struct Finish {
     float* dlogp;
     Ws* ws;
 };
-
-__device__ double block_sum(double v, double* sh) {
-    #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0;
-    #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += sh[w];
-    return v;                              // the sum, in every thread
-}
 
 __device__ __forceinline__ double softplus(double v) { return fmax(v, 0.0) + log1p(exp(-fabs(v))); }
 __device__ __forceinline__ double sigmoid(double v) {
@@ -222,56 +231,81 @@ __device__ __forceinline__ void pair_loss(const Finish& f, double h, double* los
     }
 }
 
-// One CTA per two sequences (a pair, when there is a loss): the rows' pieces
-// joined into lse, the sequences' sums in fp64 (hundreds of terms that later
-// cancel against the reference's), the loss and its gradients; the last CTA
-// to finish adds the losses up in order.
-template <class E>
-__global__ void __launch_bounds__(kThreads) lsn_seq_finish_kernel(const __grid_constant__ Rows r, const __grid_constant__ Finish f) {
-    __shared__ double sh[kThreads / 32];
+// One CTA per two sequences (a pair, when there is a loss), half of it for
+// each: the rows' pieces joined into lse, the sequences' sums in fp64 (hundreds
+// of terms that later cancel against the reference's), the loss, its gradients
+// and, for the gradient kernel of the same call, every row's factor; the last
+// CTA to finish adds the losses up in order.  Bound by its chain of loads.
+__global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __grid_constant__ Rows r, const __grid_constant__ Finish f) {
+    constexpr int kHalf = kFinThreads / 2;
+    __shared__ double sums[kFinThreads / 32];
+    __shared__ int counts[kFinThreads / 32];
+    __shared__ double lp[2];
+    __shared__ float c_row[2];
     __shared__ int is_last;
     pdl_wait();
-    double lp[2] = {0.0, 0.0};
-    int cnt[2] = {1, 1};
-    #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int q = 2 * blockIdx.x + k;
-        if (q >= r.n_seq) break;
-        const int a = max(r.start[q], 0), b = min(r.start[q + 1], r.T);
-        double sum = 0.0;
-        int n = 0;
-        for (int t = a + threadIdx.x; t < b; t += kThreads) {
-            const int y = r.targets[t];
-            if (!scored(r, t, y)) {
-                f.lse[t] = 0.f;
-                continue;
-            }
+    pdl_launch_dependents();
+    const int half = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, warp = threadIdx.x >> 5;
+    const int q = 2 * blockIdx.x + half;
+    const bool have = q < r.n_seq;
+    const int a = have ? max(r.start[q], 0) : 0, b = have ? min(r.start[q + 1], r.T) : 0;
+    double sum = 0.0;
+    int n = 0;
+    for (int t = a + tid; t < b; t += kHalf) {
+        const int y = r.targets[t];
+        float l = 0.f;
+        if (scored(r, t, y)) {
             float m = -INFINITY, s = 0.f;
+            #pragma unroll 4
             for (int i = 0; i < r.splits; ++i) {
                 const float2 p = f.part[(int64_t)t * r.splits + i];
                 join(m, s, p.x, p.y);
             }
             const double ls = log((double)s);
-            const double l = (double)Words<E>::one(reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld + y);
-            f.lse[t] = (float)((double)m + ls);
-            sum += (l - (double)m) - ls;
+            l = (float)((double)m + ls);
+            sum += ((double)f.ly[t] - (double)m) - ls;
             ++n;
         }
-        sum = block_sum(sum, sh);
-        cnt[k] = max(1, (int)block_sum((double)n, sh));
-        n = (int)block_sum((double)n, sh);
-        lp[k] = r.average ? sum / (double)cnt[k] : sum;
-        if (threadIdx.x == 0) {
-            f.logp[q] = lp[k];
+        f.lse[t] = l;
+    }
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        sums[warp] = sum;
+        counts[warp] = n;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        sum = 0.0;
+        n = 0;
+        for (int w = 0; w < kHalf / 32; ++w) {
+            sum += sums[half * (kHalf / 32) + w];
+            n += counts[half * (kHalf / 32) + w];
+        }
+        if (r.average) sum /= (double)max(n, 1);
+        lp[half] = sum;
+        counts[half * (kHalf / 32)] = max(n, 1);
+        if (have) {
+            f.logp[q] = sum;
             if (f.count) f.count[q] = n;
         }
     }
     // rows in no sequence
     if (blockIdx.x == 0) {
-        for (int t = threadIdx.x; t < min(r.start[0], r.T); t += kThreads) f.lse[t] = 0.f;
-        for (int t = max(r.start[r.n_seq], 0) + threadIdx.x; t < r.T; t += kThreads) f.lse[t] = 0.f;
+        for (int t = threadIdx.x; t < min(r.start[0], r.T); t += kFinThreads) {
+            f.lse[t] = 0.f;
+            if (f.coef) f.coef[t] = 0.f;
+        }
+        for (int t = max(r.start[r.n_seq], 0) + threadIdx.x; t < r.T; t += kFinThreads) {
+            f.lse[t] = 0.f;
+            if (f.coef) f.coef[t] = 0.f;
+        }
     }
     if (f.pairs == 0) return;
+    __syncthreads();
     if (threadIdx.x == 0) {
         const int i = blockIdx.x;
         const double ra = lp[0] - (f.ref ? f.ref[2 * i] : 0.0), rb = lp[1] - (f.ref ? f.ref[2 * i + 1] : 0.0);
@@ -285,16 +319,29 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_finish_kernel(const __grid_c
         f.loss[i] = (float)loss;
         f.dlogp[2 * i] = (float)d;
         f.dlogp[2 * i + 1] = (float)-d;
+        c_row[0] = (float)d;
+        c_row[1] = (float)-d;
         __threadfence();
         is_last = f.mean != nullptr && atomicAdd(&f.ws->done, 1) == f.pairs - 1;
         __threadfence();
     }
     __syncthreads();
+    if (f.coef) {
+        float c = c_row[half];
+        if (r.average) c /= (float)counts[half * (kHalf / 32)];
+        for (int t = a + tid; t < b; t += kHalf) f.coef[t] = scored(r, t, r.targets[t]) ? c : 0.f;
+    }
     if (!is_last) return;
     double s = 0.0;
-    for (int i = threadIdx.x; i < f.pairs; i += kThreads) s += (double)__ldcg(&f.loss[i]);
-    s = block_sum(s, sh);
+    for (int i = threadIdx.x; i < f.pairs; i += kFinThreads) s += (double)__ldcg(&f.loss[i]);
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sums[warp] = s;
+    __syncthreads();
     if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int w = 0; w < kFinThreads / 32; ++w) s += sums[w];
         *f.mean = (float)(s / f.pairs);
         f.ws->done = 0;
     }
@@ -310,63 +357,100 @@ __device__ __forceinline__ int seq_of(const Rows& r, int t) {
     return lo;
 }
 
-// dl = c ([v = y] - exp(l - lse)), zero in rows that are not scored.  Bound by
-// reading the logits and writing their gradient.
+// 16 bytes from byte offset o (0 < o < 16, even) of two neighbouring words.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (o & 8) {
+        #pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (o & 4) {
+        #pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (o & 2) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// dl = c ([v = y] - exp(l - lse)), zero in rows that are not scored.  One piece
+// of a row per CTA, the last rows first: they are what the statistics kernel
+// read last and the L2 still holds.  Bound by reading the logits and writing
+// their gradient.  Where a row of logits and its row of gradients lie
+// differently against 16 bytes, words are put together from two neighbours.
 template <class E>
 __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_constant__ Rows r, const float* lse, const float* dlogp,
-                                                                const int32_t* count, E* dl, int64_t ld_d) {
+                                                                const int32_t* count, const float* coef, E* dl, int64_t ld_d) {
     constexpr int per = Words<E>::per;
+    constexpr int U = 2;
     pdl_wait();
-    const int64_t items = (int64_t)r.T * r.splits;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int t = (int)(it / r.splits), split = (int)(it % r.splits);
-        const int y = r.targets[t];
-        const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
-        E* out = dl + (int64_t)t * ld_d;
-        const bool on = scored(r, t, y);
-        float c = 0.f, L = 0.f;
-        if (on) {
+    pdl_launch_dependents();
+    const unsigned item = gridDim.x - 1 - blockIdx.x;
+    const int t = (int)(item / (unsigned)r.splits), split = (int)(item % (unsigned)r.splits);
+    const int y = r.targets[t];
+    const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
+    E* out = dl + (int64_t)t * ld_d;
+    const bool on = scored(r, t, y);
+    float c = 0.f;
+    if (on) {
+        if (coef != nullptr) {
+            c = coef[t];
+        } else {
             const int q = seq_of(r, t);
             c = dlogp[q];
             if (r.average) c /= (float)max(count[q], 1);
-            L = lse[t];
         }
-        const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-        if (same) {
-            const Piece p = piece_of<E>(out, r.V, split, r.splits);
-            const uint4* words = reinterpret_cast<const uint4*>(row - p.mis);
-            uint4* outs = reinterpret_cast<uint4*>(out - p.mis);
-            for (int w = p.w0 + threadIdx.x; w < p.w1; w += kThreads) {
+    }
+    const float nc = -c, L = on ? lse[t] : 0.f;
+    const int o = (int)((reinterpret_cast<uintptr_t>(row) - reinterpret_cast<uintptr_t>(out)) & 15);   // 0: they lie alike
+    const Piece p = piece_of<E>(out, r.V, split, r.splits, o ? 1 : 0);
+    // with the out row's words: word w's elements start o bytes into word w of `words`
+    const uint4* words = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row - p.mis) & ~(uintptr_t)15);
+    uint4* outs = reinterpret_cast<uint4*>(out - p.mis);
+    if (!on) {
+        for (int w = p.w0 + threadIdx.x; w < p.w1; w += kThreads) __stcs(&outs[w], make_uint4(0, 0, 0, 0));
+    } else {
+        for (int w = p.w0 + threadIdx.x; w < p.w1; w += U * kThreads) {
+            uint4 x[U];
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = w + u * kThreads;
+                if (k < p.w1) x[u] = o ? shifted(words[k], words[k + 1], o) : words[k];
+            }
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = w + u * kThreads;
+                if (k >= p.w1) break;
                 float v[per];
-                if (on) {
-                    Words<E>::get(words[w], v);
-                    const int e0 = w * per - p.mis;
+                Words<E>::get(x[u], v);
+                #pragma unroll
+                for (int i = 0; i < per; ++i) v[i] = nc * ex2((v[i] - L) * kLog2e);
+                const int at = y + p.mis - k * per;                 // the target's place in this word, in one word of the row
+                if ((unsigned)at < (unsigned)per) {
                     #pragma unroll
-                    for (int i = 0; i < per; ++i) v[i] = (e0 + i == y ? c : 0.f) - c * ex2((v[i] - L) * kLog2e);
-                } else {
-                    #pragma unroll
-                    for (int i = 0; i < per; ++i) v[i] = 0.f;
+                    for (int i = 0; i < per; ++i) v[i] += i == at ? c : 0.f;
                 }
-                outs[w] = Words<E>::put(v);
+                __stcs(&outs[k], Words<E>::put(v));
             }
-            if (split == 0 && threadIdx.x < 2 * per) {
-                const int e = edge_of<E>(r.V, p.mis, threadIdx.x);
-                if (e >= 0) Words<E>::set(out + e, on ? (e == y ? c : 0.f) - c * ex2((Words<E>::one(row + e) - L) * kLog2e) : 0.f);
-            }
-        } else {
-            const int64_t a = (int64_t)r.V * split / r.splits, b = (int64_t)r.V * (split + 1) / r.splits;
-            for (int64_t e = a + threadIdx.x; e < b; e += kThreads)
-                Words<E>::set(out + e, on ? (e == y ? c : 0.f) - c * ex2((Words<E>::one(row + e) - L) * kLog2e) : 0.f);
+        }
+    }
+    if (split == 0) {
+        const int edge = p.head + r.V - p.tail;
+        if ((int)threadIdx.x < edge) {
+            const int e = (int)threadIdx.x < p.head ? (int)threadIdx.x : p.tail + (int)threadIdx.x - p.head;
+            Words<E>::set(out + e, on ? nc * ex2((Words<E>::one(row + e) - L) * kLog2e) + (e == y ? c : 0.f) : 0.f);
         }
     }
 }
 
 template <class... P, class... A>
-lsn_status launch(void (*kernel)(P...), int64_t grid, cudaStream_t st, A&&... args) {
+lsn_status launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t st, A&&... args) {
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = pdl_attr(at);
@@ -374,7 +458,7 @@ lsn_status launch(void (*kernel)(P...), int64_t grid, cudaStream_t st, A&&... ar
     return LSN_OK;
 }
 
-size_t ws_bytes_of(int64_t T, int64_t V) { return kWsHead + round_up((size_t)T * row_splits(T, V) * sizeof(float2), 256); }
+size_t ws_bytes_of(int64_t T, int64_t V) { return carve(nullptr, T, V).total; }
 
 bool off_by(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
@@ -420,33 +504,32 @@ Rows rows_of(const lsn_seq_logits* in) {
     return Rows{in->logits, in->ld, (int)in->T, (int)in->V, in->n_seq, row_splits(in->T, in->V), in->average != 0, in->targets, in->seq_start};
 }
 
-template <class E>
-lsn_status run_fwd(const Rows& r, const Finish& f, float2* part, cudaStream_t st) {
+lsn_status fwd(const lsn_seq_logits* in, Finish f, bool grad, void* ws, cudaStream_t st) {
+    const Rows r = rows_of(in);
+    const Scratch w = carve(ws, in->T, in->V);
+    f.ws = reinterpret_cast<Ws*>(ws);
+    f.part = w.part;
+    f.ly = w.ly;
+    f.coef = grad ? w.coef : nullptr;
+    const bool bf16 = in->dtype == LSN_DT_BF16;
+    TimingScope ts(LSN_K_SEQ_LOGP, (bf16 ? 2.0 : 4.0) * (double)in->T * (double)in->V + 8.0 * (double)in->T, st, r.T > 0 ? 2 : 1);
     if (r.T > 0) {
-        lsn_status s = launch(lsn_seq_stats_kernel<E>, std::min<int64_t>((int64_t)r.T * r.splits, 148 * 8), st, r, part);
+        const int64_t items = (int64_t)r.T * r.splits;
+        lsn_status s = bf16 ? launch(lsn_seq_stats_kernel<uint16_t>, items, kThreads, st, r, w.part, w.ly)
+                            : launch(lsn_seq_stats_kernel<float>, items, kThreads, st, r, w.part, w.ly);
         if (s != LSN_OK) return s;
     }
-    return launch(lsn_seq_finish_kernel<E>, ceil_div(r.n_seq, 2), st, r, f);
+    return launch(lsn_seq_finish_kernel, ceil_div(r.n_seq, 2), kFinThreads, st, r, f);
 }
 
-lsn_status fwd(const lsn_seq_logits* in, Finish f, void* ws, cudaStream_t st) {
+lsn_status bwd(const lsn_seq_logits* in, const float* lse, const float* dlogp, const int32_t* count, const float* coef, void* dlogits, int64_t ld_d,
+               cudaStream_t st) {
     const Rows r = rows_of(in);
-    f.ws = reinterpret_cast<Ws*>(ws);
-    float2* part = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHead);
-    f.part = part;
-    const double es = in->dtype == LSN_DT_BF16 ? 2.0 : 4.0;
-    TimingScope ts(LSN_K_SEQ_LOGP, es * (double)in->T * (double)in->V + 8.0 * (double)in->T, st, 2);
-    return in->dtype == LSN_DT_BF16 ? run_fwd<uint16_t>(r, f, part, st) : run_fwd<float>(r, f, part, st);
-}
-
-lsn_status bwd(const lsn_seq_logits* in, const float* lse, const float* dlogp, const int32_t* count, void* dlogits, int64_t ld_d, cudaStream_t st) {
-    const Rows r = rows_of(in);
-    const int64_t grid = std::min<int64_t>((int64_t)r.T * r.splits, 148 * 8);
-    const double es = in->dtype == LSN_DT_BF16 ? 2.0 : 4.0;
-    TimingScope ts(LSN_K_SEQ_GRAD, 2.0 * es * (double)in->T * (double)in->V, st, 1);
-    return in->dtype == LSN_DT_BF16
-               ? launch(lsn_seq_grad_kernel<uint16_t>, grid, st, r, lse, dlogp, count, (uint16_t*)dlogits, ld_d)
-               : launch(lsn_seq_grad_kernel<float>, grid, st, r, lse, dlogp, count, (float*)dlogits, ld_d);
+    const int64_t items = (int64_t)r.T * r.splits;
+    const bool bf16 = in->dtype == LSN_DT_BF16;
+    TimingScope ts(LSN_K_SEQ_GRAD, (bf16 ? 4.0 : 8.0) * (double)in->T * (double)in->V, st, 1);
+    return bf16 ? launch(lsn_seq_grad_kernel<uint16_t>, items, kThreads, st, r, lse, dlogp, count, coef, (uint16_t*)dlogits, ld_d)
+                : launch(lsn_seq_grad_kernel<float>, items, kThreads, st, r, lse, dlogp, count, coef, (float*)dlogits, ld_d);
 }
 
 lsn_status check_loss(const lsn_seq_logits* in, const double* ref, const lsn_preference* p, float* lse, double* logp, int32_t* count, float* reward,
@@ -508,7 +591,7 @@ lsn_status seq_logp_fwd(const lsn_seq_logits* in, float* lse, double* logp, int3
     f.lse = lse;
     f.logp = logp;
     f.count = count;
-    return fwd(in, f, ws, reinterpret_cast<cudaStream_t>(stream));
+    return fwd(in, f, false, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 lsn_status seq_logp_bwd(const lsn_seq_logits* in, const float* lse, const float* dlogp, const int32_t* count, void* dlogits, int64_t ld_d,
@@ -520,7 +603,7 @@ lsn_status seq_logp_bwd(const lsn_seq_logits* in, const float* lse, const float*
     if ((s = check_grad(in, lse, dlogp, count, dlogits, ld_d, "seq_logp_bwd")) != LSN_OK) return s;
     LSN_CHECK_ARG(!off_by(lse, 4) && !off_by(dlogp, 4) && !off_by(count, 4), "seq_logp_bwd: tensors must be aligned to their types");
     if ((s = check_device()) != LSN_OK) return s;
-    return bwd(in, lse, dlogp, count, dlogits, ld_d, reinterpret_cast<cudaStream_t>(stream));
+    return bwd(in, lse, dlogp, count, nullptr, dlogits, ld_d, reinterpret_cast<cudaStream_t>(stream));
 }
 
 lsn_status preference_loss_fwd(const lsn_seq_logits* in, const double* ref_logp, const lsn_preference* p, float* lse, double* logp, int32_t* count,
@@ -531,7 +614,7 @@ lsn_status preference_loss_fwd(const lsn_seq_logits* in, const double* ref_logp,
     if ((s = check_loss(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp, "preference_loss_fwd")) != LSN_OK) return s;
     if ((s = check_ws(in, ws, ws_bytes, "preference_loss_fwd")) != LSN_OK) return s;
     if ((s = check_device()) != LSN_OK) return s;
-    return fwd(in, finish_of(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp), ws, reinterpret_cast<cudaStream_t>(stream));
+    return fwd(in, finish_of(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp), false, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 lsn_status preference_loss_fwd_bwd(const lsn_seq_logits* in, const double* ref_logp, const lsn_preference* p, float* lse, double* logp, int32_t* count,
@@ -546,9 +629,9 @@ lsn_status preference_loss_fwd_bwd(const lsn_seq_logits* in, const double* ref_l
     if ((s = check_ws(in, ws, ws_bytes, who)) != LSN_OK) return s;
     if ((s = check_device()) != LSN_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((s = fwd(in, finish_of(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp), ws, st)) != LSN_OK) return s;
+    if ((s = fwd(in, finish_of(in, ref_logp, p, lse, logp, count, reward, loss, mean_loss, dlogp), true, ws, st)) != LSN_OK) return s;
     if (in->T == 0) return LSN_OK;
-    return bwd(in, lse, dlogp, count, dlogits, ld_d, st);
+    return bwd(in, lse, dlogp, count, carve(ws, in->T, in->V).coef, dlogits, ld_d, st);
 }
 
 }  // extern "C"

@@ -201,10 +201,26 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current CUDA stream as an address, without making a Stream object (a third of a small call's time)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        first = torch.cuda.current_stream().cuda_stream        # initialises CUDA
+        get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get is not None and dev is not None and get(dev()) == first:
+            _raw_stream = lambda: get(dev())                   # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

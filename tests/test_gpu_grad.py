@@ -88,6 +88,38 @@ def test_norm_and_clip(lib, sizes, types, shift, ratio):
     assert all(torch.equal(a, b) for a, b in zip(src, view))
 
 
+def test_tensors_of_one_buffer(lib):
+    """Tensors that lie end to end, in order, with gaps, out of order, and of two types side by side."""
+    import torch
+    flat = torch.randn(300000, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    half = flat[200000:].to(torch.bfloat16)
+    cuts = [(0, 7), (7, 0), (7, 50001), (50008, 3), (60000, 12345), (72345, 1), (150000, 20000), (100000, 4096), (104096, 1)]
+    src = [flat[a:a + n] for a, n in cuts] + [half[:33], half[33:5000], half[5000:5001]]
+    total = norm64(src)
+    out, outh = torch.zeros_like(flat), torch.zeros_like(half)
+    dst = [out[a:a + n] for a, n in cuts] + [outh[:33], outh[33:5000], outh[5000:5001]]
+    before = [s.clone() for s in src]
+    got, ws = run(lib, src, total / 3, dst)
+    assert abs(got - total) <= total * 2.0 ** -21
+    check(before, dst, total, total / 3)
+    covered = torch.zeros(flat.numel(), dtype=torch.bool, device="cuda")
+    for a, n in cuts:
+        covered[a:a + n] = True
+    assert bool((out[~covered] == 0).all()) and bool((outh[5001:] == 0).all())
+    apart = [torch.empty(n + 4, device="cuda")[4:] for _, n in cuts] + [torch.empty_like(d) for d in dst[-3:]]
+    run(lib, src, total / 3, apart, ws)                     # sources end to end, destinations not
+    assert all(torch.equal(x, y) for x, y in zip(apart, dst))
+
+
+def test_more_tensors_than_a_launch_takes(lib):
+    src = make([5] * 2500 + [70000], ("fp32", "bf16"), seed=3)
+    before = [s.clone() for s in src]
+    total = norm64(src)
+    got, _ = run(lib, src, total / 2)
+    assert abs(got - total) <= total * 2.0 ** -21
+    check(before, src, total, total / 2)
+
+
 def test_values_beyond_the_square_root_of_the_range(lib):
     """Squares that overflow or vanish in fp32."""
     for std in (1e25, 1e-25, 1e-38):
