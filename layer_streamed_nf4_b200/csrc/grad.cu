@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_c
         if (wide && c.lo == 0 && c.hi == kChunkBytes / es) {            // a whole chunk: four words of a thread at once
             uint4 v[kChunkBytes / 16 / kThreads];
             #pragma unroll
-            for (int u = 0; u < kChunkBytes / 16 / kThreads; ++u) v[u] = reinterpret_cast<const uint4*>(c.base)[threadIdx.x + u * kThreads];
+            for (int u = 0; u < kChunkBytes / 16 / kThreads; ++u) v[u] = __ldcs(reinterpret_cast<const uint4*>(c.base) + threadIdx.x + u * kThreads);
             #pragma unroll
             for (int u = 0; u < kChunkBytes / 16 / kThreads; ++u) __stcs(reinterpret_cast<uint4*>(dst) + threadIdx.x + u * kThreads, scaled(v[u], f, c.bf16));
             continue;
@@ -293,6 +293,7 @@ lsn_status grad_call(int n, const lsn_grad* t, bool clip, float max_norm, float*
     TimingScope ts(LSN_K_GRAD, bytes, st, clip ? 2 : 1);
     GradArgs<kMaxTensors> a;
     GradArgs<kFewTensors> few;
+    a.n = a.chunks = 0;
     auto grid_of = [&] { return std::max(1, std::min({a.chunks, 8 * sm_count(), kMaxCtas})); };
     auto is_few = [&] {                     // a small copy of the arguments, when they fit one
         if (a.n > kFewTensors) return false;

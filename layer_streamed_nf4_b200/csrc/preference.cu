@@ -14,15 +14,17 @@ namespace lsn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMinSplit = 4096;            // logits of a row that one CTA takes at least
-constexpr int kItems = 148 * 8 * 4;        // work items wanted: below as many rows, rows are split
+constexpr int kCtas = 148 * 8;             // that run at the same time
 constexpr int kFinThreads = 512;           // of the finishing kernel: half of them for each sequence of a pair
 constexpr size_t kWsHead = 256;
 
-// Pieces a row is cut into, from the shape alone.
+// Pieces a row is cut into, from the shape alone: enough that every SM has
+// work, in pieces of 4096 logits at least; and up to four times as many pieces
+// as CTAs run at once, for an even end, in pieces of 16384 at least (1021 rows
+// of 32000 in 5 pieces each took 19 us, in 2 pieces 10).
 int row_splits(int64_t T, int64_t V) {
     if (T <= 0) return 1;
-    return (int)std::max<int64_t>(1, std::min(ceil_div(kItems, T), V / kMinSplit));
+    return (int)std::max<int64_t>({1, std::min(ceil_div(kCtas, T), V / 4096), std::min(ceil_div(4 * kCtas, T), V / 16384)});
 }
 
 // The workspace behind its head: a row's pieces, its target's logit, its gradient's factor.
@@ -77,6 +79,18 @@ template <> struct Words<uint16_t> {
     static __device__ __forceinline__ uint4 put(const float (&v)[8]) {
         return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
+    static __device__ __forceinline__ uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }     // -infinity
+    template <int U>
+    static __device__ __forceinline__ float largest(const uint4 (&x)[U]) {  // two at a time
+        __nv_bfloat162 m = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        }
+        return fmaxf(__low2float(m), __high2float(m));
+    }
     static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
     static __device__ __forceinline__ void set(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 };
@@ -87,6 +101,15 @@ template <> struct Words<float> {
     }
     static __device__ __forceinline__ uint4 put(const float (&v)[4]) {
         return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+    static __device__ __forceinline__ uint4 none() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+    template <int U>
+    static __device__ __forceinline__ float largest(const uint4 (&x)[U]) {
+        float m = -INFINITY;
+        #pragma unroll
+        for (int u = 0; u < U; ++u)
+            m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(x[u].x), __uint_as_float(x[u].y))), fmaxf(__uint_as_float(x[u].z), __uint_as_float(x[u].w)));
+        return m;
     }
     static __device__ __forceinline__ float one(const float* p) { return *p; }
     static __device__ __forceinline__ void set(float* p, float v) { *p = v; }
@@ -145,31 +168,38 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
     const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
     const Piece p = piece_of<E>(row, r.V, split, r.splits, 0);
     const uint4* words = reinterpret_cast<const uint4*>(row - p.mis);
-    float m = -INFINITY, s = 0.f;
+    float m = -INFINITY, c = -INFINITY, s = 0.f;        // s: the sum of exp2(x log2 e - c), c about m log2 e
     for (int w = p.w0 + threadIdx.x; w < p.w1; w += U * kThreads) {
-        float v[U][per];
+        uint4 x[U];
         #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (w + u * kThreads < p.w1) {
-                Words<E>::get(words[w + u * kThreads], v[u]);
-            } else {
+        for (int u = 0; u < U; ++u) x[u] = w + u * kThreads < p.w1 ? words[w + u * kThreads] : Words<E>::none();
+        const float top = fmaxf(m, Words<E>::template largest<U>(x));
+        m = top;
+        if (fabsf(top) < 1e38f) {
+            // c is a number like any other: what its rounding leaves out is put right at the end
+            const float c1 = top * kLog2e;
+            if (c1 != c) s *= ex2(c - c1);
+            c = c1;
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float v[per];
+                Words<E>::get(x[u], v);
                 #pragma unroll
-                for (int i = 0; i < per; ++i) v[u][i] = -INFINITY;
+                for (int i = 0; i < per; ++i) s += ex2(fmaf(v[i], kLog2e, -c1));
+            }
+        } else {                                        // the type's lowest value, infinities, nothing yet
+            const float at = top == -INFINITY ? 0.f : top;
+            c = top * kLog2e;
+            #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float v[per];
+                Words<E>::get(x[u], v);
+                #pragma unroll
+                for (int i = 0; i < per; ++i) s += ex2((v[i] - at) * kLog2e);
             }
         }
-        float top = m;
-        #pragma unroll
-        for (int u = 0; u < U; ++u)
-            #pragma unroll
-            for (int i = 0; i < per; ++i) top = fmaxf(top, v[u][i]);
-        const float at = top == -INFINITY ? 0.f : top;
-        s *= ex2((m - at) * kLog2e);
-        m = top;
-        #pragma unroll
-        for (int u = 0; u < U; ++u)
-            #pragma unroll
-            for (int i = 0; i < per; ++i) s += ex2((v[u][i] - at) * kLog2e);
     }
+    if (fabsf(m) < 1e38f) s *= ex2(-fmaf(m, kLog2e, -c));
     if (split == 0) {
         if (threadIdx.x == 0) ly[t] = Words<E>::one(row + y);
         const int edge = p.head + r.V - p.tail;
@@ -207,10 +237,12 @@ struct Finish {
     Ws* ws;
 };
 
-__device__ __forceinline__ double softplus(double v) { return fmax(v, 0.0) + log1p(exp(-fabs(v))); }
-__device__ __forceinline__ double sigmoid(double v) {
-    const double e = exp(-fabs(v));
-    return v >= 0 ? 1.0 / (1.0 + e) : e / (1.0 + e);
+// softplus and the logistic function: their argument comes in fp64, the part
+// that is no larger than its rounding to fp32 allows is computed in fp32.
+__device__ __forceinline__ double softplus(double v) { return fmax(v, 0.0) + (double)log1pf(expf(-fabsf((float)v))); }
+__device__ __forceinline__ float sigmoid(double v) {
+    const float e = expf(-fabsf((float)v));
+    return v >= 0 ? 1.f / (1.f + e) : e / (1.f + e);
 }
 
 // Loss and its derivative with respect to the difference h of the log ratios.
@@ -219,7 +251,7 @@ __device__ __forceinline__ void pair_loss(const Finish& f, double h, double* los
     if (f.kind == LSN_PREF_SIGMOID) {
         // (without smoothing the second term is left out, not multiplied by 0: it may be infinite)
         *loss = (1.0 - e) * softplus(-z) + (e > 0.0 ? e * softplus(z) : 0.0);
-        *d = b * (e * sigmoid(z) - (1.0 - e) * sigmoid(-z));
+        *d = b * (e * (double)sigmoid(z) - (1.0 - e) * (double)sigmoid(-z));
     } else if (f.kind == LSN_PREF_HINGE) {
         const bool nan = z != z;
         *loss = nan ? z : fmax(1.0 - z, 0.0);
@@ -249,6 +281,7 @@ __global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __gri
     const int q = 2 * blockIdx.x + half;
     const bool have = q < r.n_seq;
     const int a = have ? max(r.start[q], 0) : 0, b = have ? min(r.start[q + 1], r.T) : 0;
+    const double ref0 = f.ref ? f.ref[2 * blockIdx.x] : 0.0, ref1 = f.ref ? f.ref[2 * blockIdx.x + 1] : 0.0;     // (pairs only)
     double sum = 0.0;
     int n = 0;
     for (int t = a + tid; t < b; t += kHalf) {
@@ -306,12 +339,14 @@ __global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __gri
     }
     if (f.pairs == 0) return;
     __syncthreads();
+    const int i = blockIdx.x;
     if (threadIdx.x == 0) {
-        const int i = blockIdx.x;
-        const double ra = lp[0] - (f.ref ? f.ref[2 * i] : 0.0), rb = lp[1] - (f.ref ? f.ref[2 * i + 1] : 0.0);
+        const double ra = lp[0] - ref0, rb = lp[1] - ref1;
         double loss, d;
         pair_loss(f, ra - rb, &loss, &d);
         d *= (double)f.grad_scale / f.pairs;
+        c_row[0] = (float)d;
+        c_row[1] = (float)-d;
         if (f.reward) {
             f.reward[2 * i] = (float)(f.beta * ra);
             f.reward[2 * i + 1] = (float)(f.beta * rb);
@@ -319,18 +354,20 @@ __global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __gri
         f.loss[i] = (float)loss;
         f.dlogp[2 * i] = (float)d;
         f.dlogp[2 * i + 1] = (float)-d;
-        c_row[0] = (float)d;
-        c_row[1] = (float)-d;
-        __threadfence();
-        is_last = f.mean != nullptr && atomicAdd(&f.ws->done, 1) == f.pairs - 1;
-        __threadfence();
     }
     __syncthreads();
+    if (threadIdx.x == 0) {
+        int before = -1;
+        if (f.mean != nullptr) asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(before) : "l"(&f.ws->done) : "memory");
+        is_last = before == f.pairs - 1;
+    }
     if (f.coef) {
         float c = c_row[half];
         if (r.average) c /= (float)counts[half * (kHalf / 32)];
         for (int t = a + tid; t < b; t += kHalf) f.coef[t] = scored(r, t, r.targets[t]) ? c : 0.f;
     }
+    if (f.mean == nullptr) return;
+    __syncthreads();
     if (!is_last) return;
     double s = 0.0;
     for (int i = threadIdx.x; i < f.pairs; i += kFinThreads) s += (double)__ldcg(&f.loss[i]);
@@ -384,7 +421,7 @@ template <class E>
 __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_constant__ Rows r, const float* lse, const float* dlogp,
                                                                 const int32_t* count, const float* coef, E* dl, int64_t ld_d) {
     constexpr int per = Words<E>::per;
-    constexpr int U = 2;
+    constexpr int U = 4;
     pdl_wait();
     pdl_launch_dependents();
     const unsigned item = gridDim.x - 1 - blockIdx.x;
