@@ -218,6 +218,19 @@ def _current_stream() -> int:
     return _raw_stream()
 
 
+def _dev(t, rows: bool = False) -> int | None:
+    """A device address: like _ptr, refusing tensors that are not contiguous (rows: in their last dimension) on the
+    current CUDA device."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise LsnError(LSN_ERR_INVALID_ARG, "argument", f"a tensor on {t.device} where one on the current CUDA device is needed")
+    if not (t.is_contiguous() or (rows and t.dim() > 0 and t.stride(-1) == 1)):
+        raise LsnError(LSN_ERR_INVALID_ARG, "argument", f"a tensor with strides {tuple(t.stride())} where a contiguous one is needed")
+    return t.data_ptr()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return _current_stream()
@@ -359,13 +372,13 @@ def decode_ws_bytes(projs, T: int, r: int) -> int:
 def lora_linear_decode(W: Base, x, T: int, A, B, r: int, scale: float, y, ws, ws_bytes: int, stream=None):
     """y = x W^T + scale (x A^T) B^T for T <= LSN_DECODE_MAX_T tokens, W an NF4 base read from its codes (A and B
     None: adapter off)."""
-    _check(_lib.lora_linear_decode(ctypes.byref(W), _ptr(x), T, _ptr(A), _ptr(B), r, scale, _ptr(y), _ptr(ws),
+    _check(_lib.lora_linear_decode(ctypes.byref(W), _dev(x), T, _dev(A), _dev(B), r, scale, _dev(y), _dev(ws),
                                    ws_bytes, _stream(stream)), "lora_linear_decode")
 
 
 def lora_layer_decode(projs, T: int, r: int, scale: float, ws, ws_bytes: int, stream=None):
     arr = projs if isinstance(projs, ctypes.Array) else proj_array(projs)
-    _check(_lib.lora_layer_decode(len(arr), arr, T, r, scale, _ptr(ws), ws_bytes, _stream(stream)),
+    _check(_lib.lora_layer_decode(len(arr), arr, T, r, scale, _dev(ws), ws_bytes, _stream(stream)),
            "lora_layer_decode")
 
 
@@ -375,7 +388,7 @@ def seq_logits(logits, T: int, V: int, ld: int, dtype: int, targets, n_seq: int,
                average: bool = False) -> SeqLogits:
     """Logits [T, V] (row stride ld), int32 targets [T] and int32 seq_start [n_seq + 1], all on the device; keep the
     tensors alive while the descriptor is used."""
-    return SeqLogits(_ptr(logits), T, V, ld, dtype, _ptr(targets), n_seq, _ptr(seq_start), int(bool(average)))
+    return SeqLogits(_dev(logits, rows=True), T, V, ld, dtype, _dev(targets), n_seq, _dev(seq_start), int(bool(average)))
 
 
 def preference(kind: int, beta: float, label_smoothing: float = 0.0, grad_scale: float = 1.0) -> Preference:
@@ -388,27 +401,27 @@ def seq_logp_ws_bytes(sl: SeqLogits) -> int:
 
 def seq_logp_fwd(sl: SeqLogits, lse, logp, count, ws, ws_bytes: int, stream=None):
     """lse fp32 [T], logp fp64 [n_seq] and (or None) count int32 [n_seq] of a batch of sequences."""
-    _check(_lib.seq_logp_fwd(ctypes.byref(sl), _ptr(lse), _ptr(logp), _ptr(count), _ptr(ws), ws_bytes,
+    _check(_lib.seq_logp_fwd(ctypes.byref(sl), _dev(lse), _dev(logp), _dev(count), _dev(ws), ws_bytes,
                              _stream(stream)), "seq_logp_fwd")
 
 
 def seq_logp_bwd(sl: SeqLogits, lse, dlogp, count, dlogits, ld_d: int, stream=None):
-    _check(_lib.seq_logp_bwd(ctypes.byref(sl), _ptr(lse), _ptr(dlogp), _ptr(count), _ptr(dlogits), ld_d,
+    _check(_lib.seq_logp_bwd(ctypes.byref(sl), _dev(lse), _dev(dlogp), _dev(count), _dev(dlogits), ld_d,
                              _stream(stream)), "seq_logp_bwd")
 
 
 def preference_loss_fwd(sl: SeqLogits, ref_logp, p: Preference, lse, logp, count, reward, loss, mean_loss, dlogp, ws,
                         ws_bytes: int, stream=None):
-    _check(_lib.preference_loss_fwd(ctypes.byref(sl), _ptr(ref_logp), ctypes.byref(p), _ptr(lse), _ptr(logp),
-                                    _ptr(count), _ptr(reward), _ptr(loss), _ptr(mean_loss), _ptr(dlogp), _ptr(ws),
+    _check(_lib.preference_loss_fwd(ctypes.byref(sl), _dev(ref_logp), ctypes.byref(p), _dev(lse), _dev(logp),
+                                    _dev(count), _dev(reward), _dev(loss), _dev(mean_loss), _dev(dlogp), _dev(ws),
                                     ws_bytes, _stream(stream)), "preference_loss_fwd")
 
 
 def preference_loss_fwd_bwd(sl: SeqLogits, ref_logp, p: Preference, lse, logp, count, reward, loss, mean_loss, dlogp,
                             dlogits, ld_d: int, ws, ws_bytes: int, stream=None):
-    _check(_lib.preference_loss_fwd_bwd(ctypes.byref(sl), _ptr(ref_logp), ctypes.byref(p), _ptr(lse), _ptr(logp),
-                                        _ptr(count), _ptr(reward), _ptr(loss), _ptr(mean_loss), _ptr(dlogp),
-                                        _ptr(dlogits), ld_d, _ptr(ws), ws_bytes, _stream(stream)),
+    _check(_lib.preference_loss_fwd_bwd(ctypes.byref(sl), _dev(ref_logp), ctypes.byref(p), _dev(lse), _dev(logp),
+                                        _dev(count), _dev(reward), _dev(loss), _dev(mean_loss), _dev(dlogp),
+                                        _dev(dlogits), ld_d, _dev(ws), ws_bytes, _stream(stream)),
            "preference_loss_fwd_bwd")
 
 
@@ -416,7 +429,7 @@ def preference_loss_fwd_bwd(sl: SeqLogits, ref_logp, p: Preference, lse, logp, c
 
 def grad_tensor(src, numel: int, dtype: int, dst=None) -> Grad:
     """One gradient of a norm or clip call; dst None: clipped in place."""
-    return Grad(_ptr(src), _ptr(src) if dst is None else _ptr(dst), numel, dtype)
+    return Grad(_dev(src), _dev(src) if dst is None else _dev(dst), numel, dtype)
 
 
 def grad_array(tensors) -> ctypes.Array:
@@ -433,12 +446,12 @@ def grad_ws_bytes(tensors) -> int:
 
 def grad_norm(tensors, norm, ws, ws_bytes: int, stream=None):
     arr = _grads(tensors)
-    _check(_lib.grad_norm(len(arr), arr, _ptr(norm), _ptr(ws), ws_bytes, _stream(stream)), "grad_norm")
+    _check(_lib.grad_norm(len(arr), arr, _dev(norm), _dev(ws), ws_bytes, _stream(stream)), "grad_norm")
 
 
 def grad_clip(tensors, max_norm: float, norm, ws, ws_bytes: int, stream=None):
     arr = _grads(tensors)
-    _check(_lib.grad_clip(len(arr), arr, max_norm, _ptr(norm), _ptr(ws), ws_bytes, _stream(stream)), "grad_clip")
+    _check(_lib.grad_clip(len(arr), arr, max_norm, _dev(norm), _dev(ws), ws_bytes, _stream(stream)), "grad_clip")
 
 
 def selftest_wait_timeout(limit_us: int = 1000, stream=None) -> int:

@@ -67,6 +67,12 @@ codes' bytes) stay in device memory for the whole run, so every copy moves codes
 only.  The kernels see the same arrays either way (an NF4 weight is four
 pointers), so the results are the same bits.
 
+Preference training (step(preference=...), class Preference): the forward sweep runs every layer with the
+adapters off and on, a frozen head turns the last layer's outputs into logits, the preference loss and its gradient
+follow, and the gradient enters the backward sweep as the last layer's output gradient.  step(max_norm=...) then
+scales all adapter gradients down to a largest global norm.  decode() runs up to lsnf4.LSN_DECODE_MAX_T tokens
+through the stack by the few-token calls, straight from the slots' NF4 codes: how the model just trained answers.
+
 Modes with identical kernels and launch shapes, for the bit-exactness gate
 ("Exact Layer Streaming", abstract: streamed compared with a resident run of
 the same numerics):
@@ -619,13 +625,58 @@ class Stack:
             self._join_lanes()
             self._release(l)
 
-    def step(self, accumulate: bool = False, reference: bool = False, recompute: bool = False):
+    def decode(self, adapter: bool = True):
+        """The stack's forward for T <= LSN_DECODE_MAX_T tokens (with_tokens makes such a stack) by
+        lora_layer_decode: every layer's weights are read once, as the codes in its slot; adapter=False: with the
+        adapters off.  Outputs as forward()'s: y, or y_ref with the adapters off."""
+        assert self.nf4, "the few-token calls read NF4 bases"
+        assert self.T <= lsnf4.LSN_DECODE_MAX_T, f"decode takes at most {lsnf4.LSN_DECODE_MAX_T} tokens"
+        call, n, sp = lsnf4._lib.lora_layer_decode, len(self.proj), self.stream.cuda_stream
+        if getattr(self, "_decode_ws_T", None) != self.T:
+            self._decode_bytes = lsnf4.decode_ws_bytes(self._layer_projs(0, 0), self.T, self.r)
+            with torch.cuda.stream(self.stream):
+                self._decode_ws = torch.zeros(self._decode_bytes, dtype=torch.uint8, device=self.dev)
+            self._decode_ws_T = self.T
+        order = list(range(self.L))
+        fill = self._window(order)
+        fill(self.n_slots - 1)
+        for j, l in enumerate(order):
+            addr = self._acquire(l)
+            fill(j + self.n_slots - 1)
+            st = call(n, self._layer_projs(addr, l, adapter), self.T, self.r, self.scale, self._decode_ws.data_ptr(),
+                      self._decode_bytes, sp)
+            if st:
+                lsnf4._check(st, "lora_layer_decode")
+            self._release(l)
+
+    def clip_grads(self, max_norm: float) -> torch.Tensor:
+        """Scale every dA and dB down so that their global norm is at most max_norm; the norm before that, [1] on the
+        device.  (Data-parallel replicas clip after they have summed their gradients.)"""
+        if getattr(self, "_clip", None) is None or self._clip[0] is not self.grads:
+            arr = lsnf4.grad_array([lsnf4.grad_tensor(g, g.numel(), lsnf4.LSN_DT_F32)
+                                    for k in self.grad_offsets for g in (self.dA[k], self.dB[k])])
+            nb = lsnf4.grad_ws_bytes(arr)
+            with torch.cuda.stream(self.stream):
+                ws, norm = torch.zeros(nb, dtype=torch.uint8, device=self.dev), torch.zeros(1, device=self.dev)
+            self._clip = (self.grads, arr, nb, ws, norm)
+        _, arr, nb, ws, norm = self._clip
+        lsnf4.grad_clip(arr, max_norm, norm, ws, nb, self.stream)
+        return norm
+
+    def step(self, accumulate: bool = False, reference: bool = False, recompute: bool = False,
+             preference: "Preference | None" = None, max_norm: float | None = None):
         """One training step.  reference: the forward sweep also runs every layer with the adapters off (the
         reference model of preference training, on the same stream of layers: each layer is read once for
         both forwards, so the step copies as many layers as a plain one); recompute: every layer's forward
-        runs again inside the backward sweep, as with activation checkpointing."""
-        self.forward(reference=reference)
+        runs again inside the backward sweep, as with activation checkpointing; preference: the loss whose
+        gradient enters the backward sweep (implies reference); max_norm: the largest global norm of the adapter
+        gradients (clip_grads)."""
+        self.forward(reference=reference or preference is not None)
+        if preference is not None:
+            preference.run()
         self.backward(accumulate, recompute)
+        if max_norm is not None:
+            self.clip_grads(max_norm)
 
     # ------------------------------------------------------------ facts ---
 
@@ -641,6 +692,66 @@ class Stack:
     def check_status(self):
         for ws, ln in zip(self.ws, self.lanes):
             lsnf4.ws_status(ws, ln)
+
+
+class Preference:
+    """The end of a preference training step: a frozen head [vocab, hidden] over the last layer's outputs, the
+    log-probabilities of the packed answers under the reference (adapters off) and the model, the loss of each
+    chosen / rejected pair, and its gradient as the last layer's output gradient (dY of its down projection).
+
+    targets: int32 [T], the token each row is to predict, negative where a row is not scored; seq_start: int32
+    [2 * pairs + 1] on the device, sequences 2p and 2p + 1 the chosen and the rejected answer of pair p.  One buffer
+    [T, vocab] holds the reference's logits, then the model's, then their gradient.  After run(): loss [pairs],
+    mean_loss [1], reward, logp and ref_logp [2 * pairs]."""
+
+    def __init__(self, stack: "Stack", vocab: int, targets: torch.Tensor, seq_start: torch.Tensor, beta: float,
+                 kind: int = lsnf4.LSN_PREF_SIGMOID, label_smoothing: float = 0.0, average: bool = False,
+                 grad_scale: float = 1.0, head: torch.Tensor | None = None):
+        if vocab % 64 or stack.cfg.hidden % 64:
+            raise ValueError("Preference: vocab and hidden must be multiples of 64")
+        if stack.api != "layer":
+            raise ValueError("Preference: the reference forward runs through the layer calls")
+        if not stack._distinct:
+            raise ValueError("Preference: every layer needs an output gradient of its own")
+        T, dev, n = stack.T, stack.dev, seq_start.numel() - 1
+        for t, what, size in ((targets, "targets", T), (seq_start, "seq_start", n + 1)):
+            if t.dtype != torch.int32 or t.device != dev or t.numel() != size or not t.is_contiguous():
+                raise ValueError(f"Preference: {what} must be a contiguous int32 tensor of {size} on the stack's device")
+        if n < 2 or n % 2:
+            raise ValueError("Preference: sequences come in pairs")
+        self.stack, self.targets, self.seq_start = stack, targets, seq_start
+        down = [p.name for p in stack.proj].index("down")
+        h, h_ref = stack._out(stack.y, stack.L - 1, down), stack._out(stack.y_ref, stack.L - 1, down)
+        self.head = head if head is not None else synth.device_normal((vocab, stack.cfg.hidden), 0.02, stack.seed, synth.T_EMB, 1,
+                                                                      device=dev, dtype=torch.bfloat16)
+        self.logits = torch.empty((T, vocab), dtype=torch.bfloat16, device=dev)
+        base = lsnf4.base_bf16(self.head, vocab, stack.cfg.hidden)
+        proj = lambda x: lsnf4.proj_array([lsnf4.lora_proj(base, x, None, None, y=self.logits, dY=self.logits,  # noqa: E731
+                                                           dX=stack.dY[stack.L - 1, down])])
+        self._proj, self._proj_ref = proj(h), proj(h_ref)
+        self._hws_bytes = lsnf4.layer_ws_bytes(self._proj, T, stack.r)
+        self._hws = torch.zeros(self._hws_bytes, dtype=torch.uint8, device=dev)
+        self._in = lsnf4.seq_logits(self.logits, T, vocab, vocab, lsnf4.LSN_DT_BF16, targets, n, seq_start, average)
+        self._pref = lsnf4.preference(kind, beta, label_smoothing, grad_scale)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.lse, self.count = torch.zeros(T, **f32), torch.zeros(n, dtype=torch.int32, device=dev)
+        self.logp, self.ref_logp = (torch.zeros(n, dtype=torch.float64, device=dev) for _ in range(2))
+        self.reward, self.dlogp = torch.zeros(n, **f32), torch.zeros(n, **f32)
+        self.loss, self.mean_loss = torch.zeros(n // 2, **f32), torch.zeros(1, **f32)
+        self._ws_bytes = lsnf4.seq_logp_ws_bytes(self._in)
+        self._ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=dev)
+        torch.cuda.synchronize(dev)
+
+    def run(self):
+        """After the stack's forward(reference=True): the loss, and its gradient in the stack's last dY."""
+        st, s = self.stack, self.stack.stream
+        lsnf4.lora_layer_fwd(self._proj_ref, st.T, st.r, 1.0, self._hws, self._hws_bytes, s)
+        lsnf4.seq_logp_fwd(self._in, self.lse, self.ref_logp, None, self._ws, self._ws_bytes, s)
+        lsnf4.lora_layer_fwd(self._proj, st.T, st.r, 1.0, self._hws, self._hws_bytes, s)
+        lsnf4.preference_loss_fwd_bwd(self._in, self.ref_logp, self._pref, self.lse, self.logp, self.count, self.reward,
+                                      self.loss, self.mean_loss, self.dlogp, self.logits, self.logits.shape[1], self._ws,
+                                      self._ws_bytes, s)
+        lsnf4.lora_layer_bwd(self._proj, st.T, st.r, 1.0, False, self._hws, self._hws_bytes, s)
 
 
 class HostIO:
