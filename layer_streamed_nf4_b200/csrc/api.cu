@@ -464,7 +464,7 @@ lsn_status decode_call(int n, const lsn_lora_proj* p, int64_t T, int r, float sc
     lsn_status s = check_device();
     if (s != LSN_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    TimingScope ts(LSN_K_DECODE, bytes, st, 2);
+    TimingScope ts(LSN_K_DECODE, bytes, st, decode_kernels(n, p, T, r));
     return launch_decode(n, p, (int)T, r, scale, ws, st);
 }
 

@@ -716,15 +716,267 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
         for (; used < issued; ++used) mbar_wait(&full[used % kDepth], (used / kDepth) & 1, nullptr);
 }
 
-template <int TP>
-lsn_status launch_tp(const PrepArgs& pa, const DecodeArgs& da, int grid, cudaStream_t st) {
-    static std::atomic<uint64_t> ready{0};      // devices that know the kernel's shared memory size
+// ------------------------------------------------- small calls, one launch --
+
+// Taken while its rounds (CTAs over SMs, times 1024 codes of a row at a time)
+// are few.  Measured in a graph, this launch against the two: 512 x 512, one
+// token, 2.8 and 8.0 us; 4096 x 1024, 16 tokens, 7.6 and 14.9; 4096 x 4096, one
+// token, 9.7 and 10.9 (rank 64: 14.0 and 12.9); 8192 x 2048, 8 tokens, 12.7
+// and 12.0; the seven 0.5B projections, one token, 18.6 and 14.2.
+constexpr int64_t kSmallRounds = 4;
+
+// absmax = offset + table[q] s2 with table[q] = (q - 127) / 127, [255] = 0
+__device__ __forceinline__ float absmax_of(uint32_t q, float s2, float offset) {
+    return fmaf(((float)(q == 255u ? 127u : q) - 127.f) * (1.f / 127.f), s2, offset);
+}
+
+// One 32-row tile over the whole of K per CTA: each warp takes every 16th block
+// of 64, laying x out in its registers and, ahead of the codes' arithmetic,
+// multiplying its blocks of x with A for u.  A is read once per tile, four
+// times the codes' bytes at rank 16, from the L2: that pays while a call is
+// bound by its launches and latencies.
+struct SmallProj {
+    const uint8_t* packed;
+    const uint8_t* q;
+    const float* s2;
+    const float* offset;
+    const uint16_t* x;
+    const uint16_t* A;      // NULL: adapter off
+    const uint16_t* B;
+    uint16_t* y;
+    int nb, N;
+};
+struct SmallArgs {
+    int tile0[LSN_LAYER_MAX_PROJ];      // first tile of each projection (beyond the last: INT_MAX)
+    float level[16];
+    int T, r;
+    float scale;
+    SmallProj p[LSN_LAYER_MAX_PROJ];
+};
+constexpr int kSmallThreads = 512;
+constexpr int kAhead = 2;               // blocks of a warp whose codes are in flight
+
+template <int NT>
+constexpr int small_smem(int groups) {  // table, partial sums of y and, for each 16 ranks, of u
+    return 65536 + kWarps * kRows * 8 * NT * 4 + groups * kWarps * 16 * 8 * NT * 4;
+}
+
+// The fp16 form of 16 of a token's 64 values (one lane of a quad) and its scale, as lay_out_x stores them.
+__device__ __forceinline__ float half_x(const X16& v, uint32_t (&h)[8]) {
+    uint32_t top = 0;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = v.w(i) & 0x7fff7fffu;
+        const uint32_t lo = w & 0xffffu, hi = w >> 16;
+        if (lo < 0x7f80u) top = max(top, lo);
+        if (hi < 0x7f80u) top = max(top, hi);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = min(max((int)(top >> 7) - 127, -112), 127);
+    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = v.w(i);
+        const __half2 p = __floats2half2_rn(bf16_f(w & 0xffffu) * up, __uint_as_float(w & 0xffff0000u) * up);
+        h[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kSmallThreads, 1) lsn_decode_small_kernel(const __grid_constant__ SmallArgs args) {
+    float* const part = reinterpret_cast<float*>(smem_raw + 65536);                 // [warp][row][token]
+    float* const upart = part + kWarps * kRows * 8 * NT;                            // [rank group][warp][rank][token]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int T = args.T, r = args.r;
+    int pi = 0;
+    #pragma unroll
+    for (int i = 1; i < LSN_LAYER_MAX_PROJ; ++i) pi += (int)blockIdx.x >= args.tile0[i];
+    const SmallProj& p = args.p[pi];
+    const int n0 = ((int)blockIdx.x - args.tile0[pi]) * kRows;
+    const int nb = p.nb;
+    const int64_t K = (int64_t)nb * 64;
+    {
+        const float lv = args.level[lane & 15], hi = __shfl_sync(0xffffffffu, lv, warp);
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __half2 h = __floats2half2_rn(hi, __shfl_sync(0xffffffffu, lv, i));
+            *reinterpret_cast<__half2*>(smem_raw + (warp * 16 + i) * 256 + lane * 4) = h;
+        }
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+
+    struct Codes {
+        uint2 w[4];
+        uint32_t q[4];
+        float s2[4];
+    };
+    auto load = [&](Codes& c, int b) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t blk = (int64_t)(n0 + 8 * i + g) * nb + b;
+            c.w[i] = __ldcs(reinterpret_cast<const uint2*>(p.packed + blk * 32 + t4 * 8));
+            c.q[i] = p.q[blk];
+            c.s2[i] = p.s2[blk >> 8];
+        }
+    };
+    Codes ahead[kAhead];
+    #pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (warp + k * kWarps < nb) load(ahead[k], warp + k * kWarps);
+    const float offset = *p.offset;
+
+    if (p.A != nullptr) {
+        for (int j0 = 0; j0 < r; j0 += 16) {
+            float acc[NT][4] = {};
+            #pragma unroll 2
+            for (int b = warp; b < nb; b += kWarps) {
+                const int64_t k = (int64_t)b * 64 + 16 * t4;
+                const X16 a0 = load16(p.A + (int64_t)(j0 + g) * K + k, true);
+                const X16 a1 = load16(p.A + (int64_t)(j0 + 8 + g) * K + k, j0 + 8 < r);
+                X16 xv[NT];
+                #pragma unroll
+                for (int i = 0; i < NT; ++i) xv[i] = load16(p.x + (int64_t)(g + 8 * i) * K + k, g + 8 * i < T);
+                #pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t a[4] = {a0.w(2 * m), a1.w(2 * m), a0.w(2 * m + 1), a1.w(2 * m + 1)};
+                    #pragma unroll
+                    for (int i = 0; i < NT; ++i) mma_bf16(acc[i], a, xv[i].w(2 * m), xv[i].w(2 * m + 1));
+                }
+            }
+            float* const d = upart + ((j0 / 16 * kWarps + warp) * 16 + g) * 8 * NT + 2 * t4;
+            #pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                *reinterpret_cast<float2*>(d + 8 * i) = make_float2(acc[i][0], acc[i][1]);
+                *reinterpret_cast<float2*>(d + 8 * 8 * NT + 8 * i) = make_float2(acc[i][2], acc[i][3]);
+            }
+        }
+    }
+
+    const uint32_t lane4 = lane * 4, table = smem_u32(smem_raw);
+    float acc[2][NT][4] = {};
+    for (int b0 = warp; b0 < nb; b0 += kAhead * kWarps) {
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int b = b0 + k * kWarps;
+            if (b >= nb) break;
+            uint32_t xh[NT][8];
+            float2 xs[NT];
+            #pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const float s = half_x(load16(p.x + (int64_t)(g + 8 * i) * K + (int64_t)b * 64 + 16 * t4, g + 8 * i < T), xh[i]);
+                // lane (g, t4) holds token g's scale and needs those of tokens 2 t4 and 2 t4 + 1
+                xs[i].x = __shfl_sync(0xffffffffu, s, 8 * t4);
+                xs[i].y = __shfl_sync(0xffffffffu, s, 8 * t4 + 4);
+            }
+            const Codes c = ahead[k];
+            if (b + kAhead * kWarps < nb) load(ahead[k], b + kAhead * kWarps);
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float d[NT][4] = {};
+                #pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t u = m < 2 ? c.w[2 * h].x : c.w[2 * h].y, v = m < 2 ? c.w[2 * h + 1].x : c.w[2 * h + 1].y;
+                    uint32_t a[4];
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t at = table + prmt((e & 1) ? v : u, lane4, 0x7604u | (uint32_t)(((2 * m) & 3) + (e >> 1)) << 4);
+                        asm("ld.shared.b32 %0, [%1];" : "=r"(a[e]) : "r"(at));
+                    }
+                    #pragma unroll
+                    for (int i = 0; i < NT; ++i) mma_f16(d[i], a, xh[i][2 * m], xh[i][2 * m + 1]);
+                }
+                const float lo = absmax_of(c.q[2 * h], c.s2[2 * h], offset), hi = absmax_of(c.q[2 * h + 1], c.s2[2 * h + 1], offset);
+                #pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    acc[h][i][0] = fmaf(d[i][0] * xs[i].x, lo, acc[h][i][0]);
+                    acc[h][i][1] = fmaf(d[i][1] * xs[i].y, lo, acc[h][i][1]);
+                    acc[h][i][2] = fmaf(d[i][2] * xs[i].x, hi, acc[h][i][2]);
+                    acc[h][i][3] = fmaf(d[i][3] * xs[i].y, hi, acc[h][i][3]);
+                }
+            }
+        }
+    }
+    #pragma unroll
+    for (int h = 0; h < 2; ++h)
+        #pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            float* const d = part + (warp * kRows + 16 * h + g) * 8 * NT + 8 * i + 2 * t4;
+            *reinterpret_cast<float2*>(d) = make_float2(acc[h][i][0], acc[h][i][1]);
+            *reinterpret_cast<float2*>(d + 8 * 8 * NT) = make_float2(acc[h][i][2], acc[h][i][3]);
+        }
+    __syncthreads();
+    if (p.A != nullptr) {                       // u: the warps' sums in order, left in the first warp's place
+        for (int o = threadIdx.x; o < r * 8 * NT; o += kSmallThreads) {
+            float* const d = upart + (o / (128 * NT) * kWarps * 128 * NT) + o % (128 * NT);
+            float s = 0.f;
+            #pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += d[w * 128 * NT];
+            d[0] = s;
+        }
+        __syncthreads();
+    }
+    for (int o = threadIdx.x; o < kRows * T; o += kSmallThreads) {
+        const int t = o / kRows, row = o % kRows;
+        float s = 0.f;
+        #pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += part[(w * kRows + row) * 8 * NT + t];
+        if (p.A != nullptr) {
+            const uint4* B = reinterpret_cast<const uint4*>(p.B + (int64_t)(n0 + row) * r);
+            float d = 0.f;
+            for (int j = 0; j < r; j += 8) {
+                const uint4 v = B[j / 8];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const float* u = upart + (j / 16 * kWarps * 16 + j % 16) * 8 * NT + t;
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    d = fmaf(u[2 * e * 8 * NT], bf16_f(w[e] & 0xffffu), d);
+                    d = fmaf(u[(2 * e + 1) * 8 * NT], __uint_as_float(w[e] & 0xffff0000u), d);
+                }
+            }
+            s = fmaf(args.scale, d, s);
+        }
+        p.y[(int64_t)t * p.N + n0 + row] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+    }
+}
+
+// The largest shared memory size a kernel may take, set once per device.
+template <class F>
+lsn_status allow_smem(std::atomic<uint64_t>& ready, F kernel, int bytes) {
     int dev = 0;
     LSN_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !(ready.load() >> dev & 1)) {
-        LSN_CUDA_TRY(cudaFuncSetAttribute(lsn_decode_kernel<TP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+        LSN_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
         if (dev < 64) ready.fetch_or(1ull << dev);
     }
+    return LSN_OK;
+}
+
+template <int NT>
+lsn_status launch_small(const SmallArgs& a, int tiles, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    lsn_status s = allow_smem(ready, lsn_decode_small_kernel<NT>, small_smem<NT>(4));
+    if (s != LSN_OK) return s;
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles);
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = small_smem<NT>((a.r + 15) / 16);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl_attr(at);
+    LSN_CUDA_TRY(cudaLaunchKernelEx(&cfg, lsn_decode_small_kernel<NT>, a));
+    return LSN_OK;
+}
+
+template <int TP>
+lsn_status launch_tp(const PrepArgs& pa, const DecodeArgs& da, int grid, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    lsn_status s = allow_smem(ready, lsn_decode_kernel<TP>, kSmem);
+    if (s != LSN_OK) return s;
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kPrepCtas, (unsigned)((pa.r + 15) / 16), (unsigned)da.n);
@@ -797,9 +1049,38 @@ DecodeWs carve_decode(void* ws, int n, const lsn_lora_proj* p, int64_t T, int r)
 
 }  // namespace
 
+int decode_kernels(int n, const lsn_lora_proj* p, int64_t T, int r) {
+    int64_t tiles = 0, k = 0;
+    bool on = false;
+    for (int i = 0; i < n; ++i) {
+        tiles += p[i].W.rows / kRows;
+        k = std::max(k, p[i].W.cols);
+        on = on || p[i].A != nullptr;
+    }
+    // larger ranks read more of A, more than 8 tokens do twice the arithmetic
+    const int64_t rounds = ceil_div(tiles, kMaxGrid) * ceil_div(k, 64 * kWarps) * (on && r > 16 ? 2 : 1) * (T > 8 ? 2 : 1);
+    return rounds <= kSmallRounds ? 1 : 2;
+}
+
 size_t decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r) { return carve_decode(nullptr, n, p, T, r).total; }
 
 lsn_status launch_decode(int n, const lsn_lora_proj* p, int T, int r, float scale, void* ws, cudaStream_t st) {
+    if (decode_kernels(n, p, T, r) == 1) {
+        SmallArgs a;
+        a.T = T;
+        a.r = r;
+        a.scale = scale;
+        std::copy(nf4_tables().level, nf4_tables().level + 16, a.level);
+        std::fill(a.tile0, a.tile0 + LSN_LAYER_MAX_PROJ, INT32_MAX);
+        int tile = 0;
+        for (int i = 0; i < n; ++i) {
+            const lsn_nf4_weight& f = p[i].W.nf4;
+            a.p[i] = SmallProj{f.packed, f.absmax_q, f.absmax_s2, f.offset, p[i].x, p[i].A, p[i].B, p[i].y, (int)(p[i].W.cols / 64), (int)p[i].W.rows};
+            a.tile0[i] = tile;
+            tile += (int)(p[i].W.rows / kRows);
+        }
+        return T <= 8 ? launch_small<1>(a, tile, st) : launch_small<2>(a, tile, st);
+    }
     const DecodeWs w = carve_decode(ws, n, p, T, r);
     PrepArgs pa{};
     DecodeArgs da;

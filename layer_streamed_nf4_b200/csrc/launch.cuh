@@ -166,6 +166,7 @@ lsn_status launch_lora_tgrad(const float* G, const uint16_t* X, bool out_rk, int
 lsn_status launch_lora_tgrad_batch(int n, const TgSpec* specs, int r, cudaStream_t st);
 // Few-token NF4 linears (decode.cu); arguments already checked, T in [1, LSN_DECODE_MAX_T].
 size_t decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r);
+int decode_kernels(int n, const lsn_lora_proj* p, int64_t T, int r);      // launches of a call
 lsn_status launch_decode(int n, const lsn_lora_proj* p, int T, int r, float scale, void* ws, cudaStream_t st);
 
 int down_splits(int64_t T, int64_t Kd);

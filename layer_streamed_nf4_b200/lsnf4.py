@@ -204,6 +204,14 @@ def _ptr(t) -> int | None:
 _raw_stream = None
 
 
+def _current_device() -> int:
+    """torch's current CUDA device."""
+    global _current_device
+    import torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
 def _current_stream() -> int:
     """torch's current CUDA stream as an address, without making a Stream object (a third of a small call's time)."""
     global _raw_stream
@@ -218,16 +226,19 @@ def _current_stream() -> int:
     return _raw_stream()
 
 
+def _refuse(t, what: str):
+    raise LsnError(LSN_ERR_INVALID_ARG, "argument", f"a tensor {what} where a contiguous one on the current CUDA device is needed")
+
+
 def _dev(t, rows: bool = False) -> int | None:
     """A device address: like _ptr, refusing tensors that are not contiguous (rows: in their last dimension) on the
     current CUDA device."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    import torch
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
-        raise LsnError(LSN_ERR_INVALID_ARG, "argument", f"a tensor on {t.device} where one on the current CUDA device is needed")
+    if t.get_device() != _current_device():          # -1 for a CPU tensor
+        _refuse(t, f"on {t.device}")
     if not (t.is_contiguous() or (rows and t.dim() > 0 and t.stride(-1) == 1)):
-        raise LsnError(LSN_ERR_INVALID_ARG, "argument", f"a tensor with strides {tuple(t.stride())} where a contiguous one is needed")
+        _refuse(t, f"with strides {tuple(t.stride())}")
     return t.data_ptr()
 
 
