@@ -68,7 +68,7 @@ struct DecodeProj {
     int log_g;              // G = 1 << log_g
     int steps, tiles, stages;   // stages: along K
     int counter0;           // its first counter
-    int q_align;            // rows of q start on multiples of 4, 2 or 1 bytes
+    int q_align;            // rows of q start on multiples of 16, 4, 2 or 1 bytes
 };
 struct DecodeArgs {
     CUtensorMap map[LSN_LAYER_MAX_PROJ];
@@ -275,20 +275,31 @@ struct Walk {
     }
 };
 
-// The same for the loads, with the lane's row of the second-level codes.
+// The same for the loads, with the lane's row of the second-level codes.  Rows
+// that start on 16 bytes and are walked one stage after the other are read 16
+// codes, four stages, at a time, a load ahead: four bytes a stage from 512 rows
+// are as many requests as the codes themselves.
 struct LoadWalk : Walk {
     const uint8_t* q;
     const float* s2;
     uint32_t at0;        // number of the row's first block (< 2^32: checked at launch)
     int nb, align;
+    uint4 now, next;     // align 16: the codes of the four stages that ks is in, and of the next four
 
+    __device__ __forceinline__ uint4 codes16(int first_stage) const {
+        return first_stage * kStageBlocks < nb ? *reinterpret_cast<const uint4*>(q + first_stage * kStageBlocks) : make_uint4(0, 0, 0, 0);
+    }
     __device__ __forceinline__ void rows(const DecodeArgs& a, int lane) {
         const DecodeProj& d = a.p[p];
         nb = d.nb;
-        align = d.q_align;
+        align = d.q_align == 16 && dks > 1 ? 4 : d.q_align;
         at0 = (uint32_t)(rg * kRows + lane) * (uint32_t)nb;
         q = d.q + at0;
         s2 = d.s2;
+        if (align == 16 && stages > 0) {
+            now = codes16(ks & ~3);
+            next = codes16((ks & ~3) + 4);
+        }
     }
 };
 
@@ -299,13 +310,22 @@ struct AmRaw {
     float s2a, s2b;
     int cut;
 };
-__device__ __forceinline__ AmRaw load_am(const LoadWalk& w, int ks) {
+__device__ __forceinline__ AmRaw load_am(LoadWalk& w, int ks) {
     AmRaw r;
     const int b0 = ks * kStageBlocks;
     const uint32_t at = w.at0 + (uint32_t)b0;
     const uint8_t* q = w.q + b0;
     r.cut = kStageBlocks;
     r.s2a = r.s2b = w.s2[at >> 8];
+    if (w.align == 16) {
+        const int i = ks & 3;
+        r.q = i == 0 ? w.now.x : i == 1 ? w.now.y : i == 2 ? w.now.z : w.now.w;
+        if (i == 3) {
+            w.now = w.next;
+            w.next = w.codes16(ks + 5);
+        }
+        return r;
+    }
     if (w.align == 4) {                         // nb % 4 == 0: four blocks, all of one group
         r.q = *reinterpret_cast<const uint32_t*>(q);
         return r;
@@ -560,18 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
             if (dead) continue;
             ++used;
             stsf4(am_sh + lane * 16, absmax4(raw[0], offset));
-            // the stage's codes, all into registers: the slot is free again before the arithmetic begins
             const uint32_t st = ring + slot * kStageBytes;
-            uint2 cw[kStageBlocks][4];
-            #pragma unroll
-            for (int j = 0; j < kStageBlocks; ++j)
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) cw[j][i] = lds64(st + (piece ^ (32 * j)) + i * 1024);
-            __syncwarp();
-            #pragma unroll
-            for (int i = 0; i + 1 < kDepth; ++i) raw[i] = raw[i + 1];
-            load_next(raw[kDepth - 1]);
             if constexpr (TP == 2) {
+                // the stage's codes, all into registers: the slot is free again before the arithmetic begins
+                uint2 cw[kStageBlocks][4];
+                #pragma unroll
+                for (int j = 0; j < kStageBlocks; ++j)
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) cw[j][i] = lds64(st + (piece ^ (32 * j)) + i * 1024);
+                __syncwarp();
+                #pragma unroll
+                for (int i = 0; i + 1 < kDepth; ++i) raw[i] = raw[i + 1];
+                load_next(raw[kDepth - 1]);
                 float c[2][4] = {};
                 #pragma unroll
                 for (int j = 0; j < kStageBlocks; ++j) {
@@ -600,24 +620,28 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
                     acc[h][0][3] = fmaf(c[h][3] * xs2.y, hi, acc[h][0][3]);
                 }
             } else {
+                // a rolled loop: unrolled, or with the next block's x read ahead, registers spill and moves
+                // add up (8B layer, 8 tokens: 54 and 51 us against 50)
+                __syncwarp();                   // am_sh is written
                 const int nj = min(kStageBlocks, nb - b0);
-                #pragma unroll
-                for (int j = 0; j < kStageBlocks; ++j) {
-                    if (j >= nj) break;
+                #pragma unroll 1
+                for (int j = 0; j < nj; ++j) {
                     uint4 xa[NT], xc[NT];
                     float2 xs[NT];
                     #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
+                    for (int i = 0; i < NT; ++i) {  // lane (g, t4): a quarter of token g
                         xa[i] = xc[i] = make_uint4(0, 0, 0, 0);
                         if (g + 8 * i < T) {
-                            xa[i] = *reinterpret_cast<const uint4*>(xb + j * (TP * 128) + i * 512);
-                            xc[i] = *reinterpret_cast<const uint4*>(xb + j * (TP * 128) + i * 512 + TP * 64);
+                            xa[i] = *reinterpret_cast<const uint4*>(xb + i * 512);
+                            xc[i] = *reinterpret_cast<const uint4*>(xb + i * 512 + TP * 64);
                         }
-                        xs[i] = *reinterpret_cast<const float2*>(xsb + j * (TP * 4) + i * 32);
+                        xs[i] = *reinterpret_cast<const float2*>(xsb + i * 32);
                     }
+                    xb += TP * 128;
+                    xsb += TP * 4;
                     #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint2 u = cw[j][2 * h], v = cw[j][2 * h + 1];
+                        const uint2 u = lds64(st + (piece ^ (32 * j)) + h * 2048), v = lds64(st + (piece ^ (32 * j)) + h * 2048 + 1024);
                         const float lo = ldsf(am_sh + (16 * h + rowp) * 16 + j * 4), hi = ldsf(am_sh + (16 * h + 8 + rowp) * 16 + j * 4);
                         float c[NT][4] = {};
                         uint32_t a[4];
@@ -642,6 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
                         }
                     }
                 }
+                __syncwarp();                   // every lane has read the slot
+                #pragma unroll
+                for (int i = 0; i + 1 < kDepth; ++i) raw[i] = raw[i + 1];
+                load_next(raw[kDepth - 1]);
             }
             __syncwarp();                       // every lane has read am_sh
         }
@@ -1107,7 +1135,7 @@ lsn_status launch_decode(int n, const lsn_lora_proj* p, int T, int r, float scal
         const Cut c = cut_of(q.W.rows, q.W.cols, per_cta);
         const uintptr_t qa = reinterpret_cast<uintptr_t>(f.absmax_q) | (uintptr_t)nb;
         da.p[i] = DecodeProj{f.absmax_q, f.absmax_s2, f.offset, w.xf[lead], w.xs[lead], off ? nullptr : w.u[i], q.B, q.y, nb, (int)q.W.rows,
-                             c.log_g, c.steps, c.tiles, (int)ceil_div(nb, kStageBlocks), (int)counters, qa % 4 == 0 ? 4 : qa % 2 == 0 ? 2 : 1};
+                             c.log_g, c.steps, c.tiles, (int)ceil_div(nb, kStageBlocks), (int)counters, qa % 16 == 0 ? 16 : qa % 4 == 0 ? 4 : qa % 2 == 0 ? 2 : 1};
         da.step0[i] = (int)total;
         // the packed codes as 16-bit elements: rows of K / 4, boxes of 64 x 32
         lsn_status s = make_tmap_2d(&da.map[i], f.packed, q.W.cols / 4, q.W.rows, q.W.cols / 4, 64, kRows, false);
