@@ -155,7 +155,9 @@ template <int TP>
 __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __grid_constant__ PrepArgs args) {
     constexpr int NT = (TP + 7) / 8;
     __shared__ float part[kPrepWarps][16][8 * NT];
-    __shared__ float mine[16][8 * NT];
+    __shared__ float sums[kPrepCtas][16 * 8 * NT];       // of CTA 0: every CTA's sums
+    const bool dots = args.p[blockIdx.z].A != nullptr;      // the same for the whole cluster
+    if (dots) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");    // started: waited for before writing to CTA 0
     pdl_wait();
     pdl_launch_dependents();
     for (int i = ((blockIdx.z * gridDim.y + blockIdx.y) * kPrepCtas + blockIdx.x) * kPrepThreads + threadIdx.x; i < args.n_counters;
@@ -166,10 +168,10 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int j0 = blockIdx.y * 16;
     const bool lays = p.xf != nullptr && blockIdx.y == 0;
-    const bool dots = p.A != nullptr;
     const int64_t K = (int64_t)p.nb * 64;
     float acc[NT][4] = {};
     if (lays || dots) {
+        #pragma unroll 2
         for (int b = blockIdx.x * kPrepWarps + warp; b < p.nb; b += kPrepCtas * kPrepWarps) {
             const int64_t k = (int64_t)b * 64 + 16 * t4;
             X16 xv[NT];
@@ -204,28 +206,26 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
         part[warp][g + 8][8 * i + 2 * t4 + 1] = acc[i][3];
     }
     __syncthreads();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    // each CTA's sums go into CTA 0's shared memory; it alone waits for them
+    const uint32_t rank = cluster_ctarank();
     for (int i = threadIdx.x; i < 16 * 8 * NT; i += kPrepThreads) {
         float s = 0.f;
         #pragma unroll
         for (int w = 0; w < kPrepWarps; ++w) s += (&part[w][0][0])[i];
-        (&mine[0][0])[i] = s;
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&sums[rank][i]), 0)), "f"(s) : "memory");
     }
-    cluster_sync_all();
-    if (cluster_ctarank() == 0) {
-        for (int i = threadIdx.x; i < 16 * 8 * NT; i += kPrepThreads) {
-            const int j = j0 + i / (8 * NT), t = i % (8 * NT);
-            if (j >= r || t >= T) continue;
-            float s = 0.f;
-            #pragma unroll
-            for (int c = 0; c < kPrepCtas; ++c) {
-                float v;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&mine[0][0] + i), c)) : "memory");
-                s += v;
-            }
-            p.u[(int64_t)t * r + j] = s;
-        }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int i = threadIdx.x; i < 16 * 8 * NT; i += kPrepThreads) {
+        const int j = j0 + i / (8 * NT), t = i % (8 * NT);
+        if (j >= r || t >= T) continue;
+        float s = 0.f;
+        #pragma unroll
+        for (int c = 0; c < kPrepCtas; ++c) s += sums[c][i];
+        p.u[(int64_t)t * r + j] = s;
     }
-    cluster_sync_all();     // the partial sums stay readable until CTA 0 has them
 }
 
 extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
                 #pragma unroll
                 for (int i = 0; i + 1 < kDepth; ++i) raw[i] = raw[i + 1];
                 load_next(raw[kDepth - 1]);
-                float c[2][4] = {};
+                float c[2][4] = {}, e[2][4] = {};       // two chains of MMAs each
                 #pragma unroll
                 for (int j = 0; j < kStageBlocks; ++j) {
                     const uint32_t on = (g >> 1) == j ? 0xffffffffu : 0u;
@@ -604,13 +604,17 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
                         operand<0>(a, u.x, v.x, lane4);
                         mma_f16(c[h], a, bx[0], bx[1]);
                         operand<2>(a, u.x, v.x, lane4);
-                        mma_f16(c[h], a, bx[2], bx[3]);
+                        mma_f16(e[h], a, bx[2], bx[3]);
                         operand<0>(a, u.y, v.y, lane4);
-                        mma_f16(c[h], a, bx[4], bx[5]);
+                        mma_f16(e[h], a, bx[4], bx[5]);
                         operand<2>(a, u.y, v.y, lane4);
                         mma_f16(c[h], a, bx[6], bx[7]);
                     }
                 }
+                #pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) c[h][i] += e[h][i];
                 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float lo = ldsf(am_sh + (16 * h + rowp) * 16 + t4 * 4), hi = ldsf(am_sh + (16 * h + 8 + rowp) * 16 + t4 * 4);
