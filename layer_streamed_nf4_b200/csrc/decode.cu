@@ -17,7 +17,9 @@ namespace {
 
 constexpr int kPrepThreads = 512;
 constexpr int kPrepWarps = kPrepThreads / 32;
-constexpr int kPrepCtas = 8;       // CTAs (one cluster) that share the contraction of one projection's u
+constexpr int kPrepCtas = 8;       // CTAs (one cluster) that share the contraction of a slice of one projection's u
+constexpr int kSliceBlocks = kPrepCtas * kPrepWarps;       // a block of 64 a warp; longer rows are cut into
+constexpr int kMaxSlices = 4;                              // up to so many slices, then warps take more blocks
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 32;          // output rows of a warp's tile: two 16-row MMA operands
@@ -40,10 +42,11 @@ constexpr uint32_t kSmem = kBarAt + kWarps * kDepth * 8 - 1024;        // the wi
 struct PrepProj {
     const uint16_t* x;
     const uint16_t* A;      // NULL: adapter off
-    float* u;               // [T, r]
+    float* u;               // [slices, T, r]
     __half* xf;             // [K/64, 2, TP, 32] fp16, or NULL when another projection lays the same x out
     float* xs;              // [K/64, TP] scale of each fp16 block
     int nb;                 // K / 64
+    int slices;
 };
 struct PrepArgs {
     PrepProj p[LSN_LAYER_MAX_PROJ];
@@ -62,6 +65,7 @@ struct DecodeProj {
     const __half* xf;
     const float* xs;
     const float* u;         // NULL: adapter off
+    int slices;             // of u
     const uint16_t* B;
     uint16_t* y;
     int nb, N;
@@ -156,23 +160,24 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
     constexpr int NT = (TP + 7) / 8;
     __shared__ float part[kPrepWarps][16][8 * NT];
     __shared__ float sums[kPrepCtas][16 * 8 * NT];       // of CTA 0: every CTA's sums
-    const bool dots = args.p[blockIdx.z].A != nullptr;      // the same for the whole cluster
+    const int slice = blockIdx.x / kPrepCtas, slices = args.p[blockIdx.z].slices;
+    const bool dots = args.p[blockIdx.z].A != nullptr && slice < slices;       // the same for the whole cluster
     if (dots) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");    // started: waited for before writing to CTA 0
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = ((blockIdx.z * gridDim.y + blockIdx.y) * kPrepCtas + blockIdx.x) * kPrepThreads + threadIdx.x; i < args.n_counters;
-         i += gridDim.z * gridDim.y * kPrepCtas * kPrepThreads)
+    for (int i = ((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * kPrepThreads + threadIdx.x; i < args.n_counters;
+         i += gridDim.z * gridDim.y * gridDim.x * kPrepThreads)
         args.counters[i] = 0;
     const PrepProj& p = args.p[blockIdx.z];
     const int T = args.T, r = args.r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int j0 = blockIdx.y * 16;
-    const bool lays = p.xf != nullptr && blockIdx.y == 0;
+    const bool lays = p.xf != nullptr && blockIdx.y == 0 && slice < slices;
     const int64_t K = (int64_t)p.nb * 64;
     float acc[NT][4] = {};
     if (lays || dots) {
         #pragma unroll 2
-        for (int b = blockIdx.x * kPrepWarps + warp; b < p.nb; b += kPrepCtas * kPrepWarps) {
+        for (int b = blockIdx.x * kPrepWarps + warp; b < p.nb; b += slices * kSliceBlocks) {
             const int64_t k = (int64_t)b * 64 + 16 * t4;
             X16 xv[NT];
             #pragma unroll
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
         float s = 0.f;
         #pragma unroll
         for (int c = 0; c < kPrepCtas; ++c) s += sums[c][i];
-        p.u[(int64_t)t * r + j] = s;
+        p.u[((int64_t)slice * T + t) * r + j] = s;
     }
 }
 
@@ -417,7 +422,12 @@ __device__ __forceinline__ void add_adapter(const DecodeArgs& a, const DecodePro
             #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (t >= T) break;
-                const float2 u = *reinterpret_cast<const float2*>(p.u + t * r + j);
+                float2 u = *reinterpret_cast<const float2*>(p.u + t * r + j);
+                for (int k = 1; k < p.slices; ++k) {
+                    const float2 v = *reinterpret_cast<const float2*>(p.u + (k * T + t) * r + j);
+                    u.x += v.x;
+                    u.y += v.y;
+                }
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float d = fmaf(u.x, __uint_as_float(b[i] << 16), u.y * __uint_as_float(b[i] & 0xffff0000u));
@@ -434,7 +444,14 @@ __device__ __forceinline__ void add_adapter(const DecodeArgs& a, const DecodePro
             for (int k = 0; k < 2 * NT; ++k) {
                 const int t = 8 * (k / 2) + 2 * t4 + (k & 1);
                 if (t >= T) continue;
-                const float4 u = *reinterpret_cast<const float4*>(p.u + t * r + j);
+                float4 u = *reinterpret_cast<const float4*>(p.u + t * r + j);
+                for (int n = 1; n < p.slices; ++n) {
+                    const float4 v = *reinterpret_cast<const float4*>(p.u + (n * T + t) * r + j);
+                    u.x += v.x;
+                    u.y += v.y;
+                    u.z += v.z;
+                    u.w += v.w;
+                }
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float d = u.x * __uint_as_float(b[i].x << 16);
@@ -1009,9 +1026,11 @@ lsn_status launch_tp(const PrepArgs& pa, const DecodeArgs& da, int grid, cudaStr
     static std::atomic<uint64_t> ready{0};
     lsn_status s = allow_smem(ready, lsn_decode_kernel<TP>, kSmem);
     if (s != LSN_OK) return s;
+    int slices = 1;
+    for (int i = 0; i < da.n; ++i) slices = std::max(slices, pa.p[i].slices);
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kPrepCtas, (unsigned)((pa.r + 15) / 16), (unsigned)da.n);
+    cfg.gridDim = dim3((unsigned)(kPrepCtas * slices), (unsigned)((pa.r + 15) / 16), (unsigned)da.n);
     cfg.blockDim = dim3(kPrepThreads);
     cfg.stream = st;
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1071,7 +1090,7 @@ DecodeWs carve_decode(void* ws, int n, const lsn_lora_proj* p, int64_t T, int r)
     w.part = reinterpret_cast<float*>(take((size_t)kMaxGrid * 2 * kWarps * kRows * LSN_DECODE_MAX_T * 4));
     for (int i = 0; i < n; ++i) {
         const size_t K = (size_t)p[i].W.cols;
-        w.u[i] = reinterpret_cast<float*>(take((size_t)T * r * 4));
+        w.u[i] = reinterpret_cast<float*>(take((size_t)kMaxSlices * T * r * 4));
         w.xf[i] = reinterpret_cast<__half*>(take((size_t)pad_tokens(T) * K * 2));
         w.xs[i] = reinterpret_cast<float*>(take(K / 64 * LSN_DECODE_MAX_T * 4));
     }
@@ -1134,11 +1153,12 @@ lsn_status launch_decode(int n, const lsn_lora_proj* p, int T, int r, float scal
         while (p[lead].x != q.x || p[lead].W.cols != q.W.cols) ++lead;
         const bool off = q.A == nullptr;
         const int nb = (int)(q.W.cols / 64);
-        pa.p[i] = PrepProj{q.x, q.A, w.u[i], lead == i ? w.xf[i] : nullptr, w.xs[i], nb};
+        const int slices = (int)std::min<int64_t>(ceil_div(nb, kSliceBlocks), kMaxSlices);
+        pa.p[i] = PrepProj{q.x, q.A, w.u[i], lead == i ? w.xf[i] : nullptr, w.xs[i], nb, slices};
         const lsn_nf4_weight& f = q.W.nf4;
         const Cut c = cut_of(q.W.rows, q.W.cols, per_cta);
         const uintptr_t qa = reinterpret_cast<uintptr_t>(f.absmax_q) | (uintptr_t)nb;
-        da.p[i] = DecodeProj{f.absmax_q, f.absmax_s2, f.offset, w.xf[lead], w.xs[lead], off ? nullptr : w.u[i], q.B, q.y, nb, (int)q.W.rows,
+        da.p[i] = DecodeProj{f.absmax_q, f.absmax_s2, f.offset, w.xf[lead], w.xs[lead], off ? nullptr : w.u[i], slices, q.B, q.y, nb, (int)q.W.rows,
                              c.log_g, c.steps, c.tiles, (int)ceil_div(nb, kStageBlocks), (int)counters, qa % 16 == 0 ? 16 : qa % 4 == 0 ? 4 : qa % 2 == 0 ? 2 : 1};
         da.step0[i] = (int)total;
         // the packed codes as 16-bit elements: rows of K / 4, boxes of 64 x 32
