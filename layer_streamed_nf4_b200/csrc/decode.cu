@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
             if (ks >= cur.stages) continue;
             const int slot = used % kDepth;
             const int b0 = ks * kStageBlocks;
-            const char* xb = xf + (uint32_t)(b0 * (TP * 128));
-            const char* xsb = xsp + (uint32_t)(b0 * (TP * 4));
+            const char* xb = xf + (size_t)b0 * (TP * 128);
+            const char* xsb = xsp + (size_t)b0 * (TP * 4);
             uint4 xa2 = make_uint4(0, 0, 0, 0), xc2 = xa2;
             float2 xs2 = make_float2(0.f, 0.f);
             if constexpr (TP == 2) {            // ahead of the wait
@@ -1166,7 +1166,7 @@ lsn_status launch_decode(int n, const lsn_lora_proj* p, int T, int r, float scal
         if (s != LSN_OK) return s;
         total += (int64_t)c.steps * c.tiles;
         counters += (int64_t)c.tiles * kWarps;
-        if (total > INT32_MAX / 2 || q.W.rows * nb > (int64_t)UINT32_MAX) return fail(LSN_ERR_UNSUPPORTED, "lora_layer_decode: weights too large");
+        if (total > INT32_MAX / 2 || counters > INT32_MAX || q.W.rows * nb > (int64_t)UINT32_MAX) return fail(LSN_ERR_UNSUPPORTED, "lora_layer_decode: weights too large");
     }
     const int grid = (int)std::min<int64_t>({total, sm_count(), kMaxGrid});
     da.per = (int)(total / grid);

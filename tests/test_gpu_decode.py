@@ -398,3 +398,38 @@ def test_timing_counts_the_calls(lib, K, kernels):
     t = lib.timing_read()
     lib.timing_enable(False)
     assert t["decode"]["launches"] == 1 and t["decode"]["kernels"] == kernels and t["decode"]["ms"] > 0
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_offsets_beyond_32_bits(lib, T):
+    """Rows of 2^27 + 128 weights: 16 tokens of them are over 2^32 bytes, laid out and read.  x is zero but for the
+    first and the last block, so that these alone make the outputs."""
+    import torch
+    K, N = (1 << 27) + 128, 64
+    nb = K // 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    packed = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    q = torch.randint(100, 156, (N, nb), dtype=torch.uint8, device="cuda", generator=g)
+    s2 = torch.rand((N * nb + 255) // 256, device="cuda", generator=g) * 0.01
+    off = torch.full((1,), 0.05, device="cuda")
+    base = lib.base_nf4(lib.make_nf4_weight(N, K, packed, q, s2, off))
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    x[:, :64].normal_(generator=g)
+    x[:, -64:].normal_(generator=g)
+    y = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    d = lib.lora_proj(base, x, None, None, y=y)
+    ws, n = _ws(lib, [d], T, 8)
+    lib.lora_linear_decode(base, x, T, None, None, 8, 1.0, y, ws, n)
+    torch.cuda.synchronize()
+    lib.ws_status(ws)
+    lv = torch.from_numpy(_levels(lib)).cuda()
+    want, tol = 0.0, 0.0
+    for b in (0, nb - 1):
+        c = packed[:, 32 * b:32 * b + 32].long()
+        blk = torch.arange(N, device="cuda") * nb + b
+        am = (q[:, b].double() - 127) / 127 * s2[blk // 256].double() + 0.05
+        W = torch.stack([lv[c // 16], lv[c % 16]], 2).view(N, 64) * am[:, None]
+        want = want + x[:, 64 * b:64 * b + 64].double() @ W.T
+        tol = tol + x[:, 64 * b:64 * b + 64].double().abs() @ W.abs().T
+    tol = tol * (2.0 ** -11 + 300 * 2.0 ** -24) + want.abs() * 2.0 ** -8
+    assert bool(((y.double() - want).abs() <= tol).all())
