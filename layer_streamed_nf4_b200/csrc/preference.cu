@@ -21,7 +21,7 @@ constexpr size_t kWsHead = 256;
 // Pieces a row is cut into, from the shape alone: enough that every SM has
 // work, in pieces of 4096 logits at least; and up to four times as many pieces
 // as CTAs run at once, for an even end, in pieces of 16384 at least (1021 rows
-// of 32000 in 5 pieces each took 19 us, in 2 pieces 10).
+// of 32000 in 5 pieces each took 19 us, in 2 pieces 12.5).
 int row_splits(int64_t T, int64_t V) {
     if (T <= 0) return 1;
     return (int)std::max<int64_t>({1, std::min(ceil_div(kCtas, T), V / 4096), std::min(ceil_div(4 * kCtas, T), V / 16384)});
@@ -150,11 +150,14 @@ __device__ __forceinline__ Piece piece_of(const void* row, int V, int split, int
     return p;
 }
 
-// (m, s) of one piece of one row per CTA, and the target's logit.  Bound by
-// reading the logits; each thread keeps four 16-byte loads in flight, and the
-// special-function unit (one exp2 a logit) is busy for about two thirds of
-// the time that takes.  CTAs are handed out as others finish: rows that are
-// not scored cost nothing.
+// (m, s) of one piece of one row per CTA, and the target's logit.  Each thread
+// keeps four 16-byte loads in flight; maxima of bf16 are taken two at a time.
+// Bound by DRAM and, nearly as much, the special-function unit (one exp2 a
+// logit): 2048 x 151936 bf16, three quarters scored, 77 us, 6.1 TB/s.  With
+// exp2((x - m) log2 e) in two instructions it took 94 us, with the words behind
+// a piece's end computed like others 81 (3 pieces of 6.2 rounds took 7 each);
+// two products or sums in one instruction (f32x2) changed nothing.  CTAs are
+// handed out as others finish: rows that are not scored cost nothing.
 template <class E>
 __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_constant__ Rows r, float2* part, float* ly) {
     constexpr int per = Words<E>::per;
@@ -173,6 +176,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
         uint4 x[U];
         #pragma unroll
         for (int u = 0; u < U; ++u) x[u] = w + u * kThreads < p.w1 ? words[w + u * kThreads] : Words<E>::none();
+        const int first = w - (int)(threadIdx.x & 31);      // of the warp's words; those past the end are -infinity
         const float top = fmaxf(m, Words<E>::template largest<U>(x));
         m = top;
         if (fabsf(top) < 1e38f) {
@@ -182,6 +186,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
             c = c1;
             #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (u > 0 && first + u * kThreads >= p.w1) break;
                 float v[per];
                 Words<E>::get(x[u], v);
                 #pragma unroll
@@ -414,8 +419,9 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) 
 
 // dl = c ([v = y] - exp(l - lse)), zero in rows that are not scored.  One piece
 // of a row per CTA, the last rows first: they are what the statistics kernel
-// read last and the L2 still holds.  Bound by reading the logits and writing
-// their gradient.  Where a row of logits and its row of gradients lie
+// read last and the L2 still holds (2048 x 151936 bf16: 4 us of 269 for the
+// whole loss).  Bound by reading the logits and writing their gradient: 171 us
+// there, 6.4 TB/s.  Where a row of logits and its row of gradients lie
 // differently against 16 bytes, words are put together from two neighbours.
 template <class E>
 __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_constant__ Rows r, const float* lse, const float* dlogp,
