@@ -12,6 +12,13 @@
  *                               Laptop? (I Did the Math)", 2:19-2:29);
  *   lora_linear_fwd / _bwd      y = x W^T + s (x A^T) B^T and its gradients
  *                               for x, A, B (same video, 1:36-1:58);
+ *   lora_linear_decode, lora_layer_decode
+ *                               the same linears for a handful of tokens,
+ *                               straight from the codes;
+ *   seq_logp_*, preference_loss_*
+ *                               log-probabilities of packed answers and the
+ *                               loss of preference training, with gradients;
+ *   grad_norm, grad_clip        the adapter gradients' global norm;
  *   layer_pool_*                the VRAM layer pool fed from pinned host RAM,
  *                               prefetching the next layer on a side stream
  *                               (same video, 7:11-7:42; the sourcefeed article
@@ -31,7 +38,8 @@
  *    bit patterns.  Pointers passed to a compute call must stay valid until
  *    the work enqueued on the stream has finished.
  *  - Every tensor pointer must be 16-byte aligned (the tensor-memory-access
- *    unit reads rows in 16-byte units).
+ *    unit reads rows in 16-byte units), but for the calls that state their own
+ *    alignments (the preference loss, the gradient norm).
  *  - Results are deterministic: the same inputs and shapes give the same bits,
  *    independent of pointers, streams or what ran before.
  */
@@ -319,7 +327,8 @@ size_t lsn_decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r);
 lsn_status lora_linear_decode(const lsn_base* W, const uint16_t* x, int64_t T, const uint16_t* A, const uint16_t* B,
                               int r, float scale, uint16_t* y, void* ws, size_t ws_bytes, lsn_stream_t stream);
 
-/* All projections of a layer (n <= LSN_LAYER_MAX_PROJ) in the same two launches. */
+/* All projections of a layer (n <= LSN_LAYER_MAX_PROJ) together, in one launch
+ * or two as their shapes have it. */
 lsn_status lora_layer_decode(int n, const lsn_lora_proj* p, int64_t T, int r, float scale, void* ws, size_t ws_bytes,
                              lsn_stream_t stream);
 
@@ -516,7 +525,10 @@ lsn_status lsn_timing_read(lsn_kernel_timing* out);
  *                      (barriers, tensor memory, tensor-map prefetch) overlaps
  *                      the tail of the kernel before it on the same stream;
  *                      every kernel still waits for its predecessor to finish
- *                      before it reads or writes global memory.  0: ordinary
+ *                      before it reads or writes global memory (the few-token
+ *                      linears' main kernel reads its weights while the
+ *                      preparation kernel of the same call runs, which itself
+ *                      began after everything before the call).  0: ordinary
  *                      stream-ordered launches.
  *   LSN_OPT_GEMM_MIN_UNITS 1: a GEMM whose tiles take R rounds over all the
  *                      SMs runs on the fewest SMs that still finish in R

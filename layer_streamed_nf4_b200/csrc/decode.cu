@@ -1,8 +1,17 @@
 // NF4 LoRA linears for a handful of tokens (1 to LSN_DECODE_MAX_T):
 //   y[t, n] = sum_b a[n, b] sum_{k in block b} level[code[n, k]] x[t, k] + s sum_j u[t, j] B[n, j],   u = x A^T,
 // straight from the packed codes: every code is read once and no bf16 copy of
-// W is made.  Two kernels: lsn_decode_prep_kernel makes u and lays x out for
-// the tensor cores, lsn_decode_kernel streams the codes.
+// W is made.  Calls of many rounds take two kernels: lsn_decode_prep_kernel
+// makes u and lays x out for the tensor cores, lsn_decode_kernel streams the
+// codes.  Calls of few take one, lsn_decode_small_kernel.
+//
+// Decoding.  A byte is a pair of codes and an entry of a 256-entry table of
+// pairs of fp16 levels in shared memory: a byte permute and a 4-byte load for
+// two weights (by permutes of a table in registers it takes 5.5 instructions,
+// and those issue at half the rate of others).  The pair is an A register of
+// mma.sync m16n8k16: with at most 16 columns the warp-level instruction, 0.475
+// a clock and SM, costs a sixth of the lookups' time, and a tcgen05 tile would
+// stand nearly empty.  The levels in fp16 carry 11 significant bits (2^-11).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -94,8 +103,8 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float bf16_f(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
@@ -118,12 +127,12 @@ __device__ __forceinline__ X16 load16(const uint16_t* p, bool on) {
 }
 
 // One block of 64 x values of one token, 16 per lane of a quad, as fp16 times
-// a power of two of the block's own: bf16 has 8 significant bits and fp16 11,
-// so a value down to 2^-28 of the block's largest is kept exactly or to
-// 2^-24 of 2^-14 of the largest, below what an fp32 sum keeps; the power of
-// two puts the largest finite value into [2^14, 2^15).  Infinities and NaN
-// stay what they are.
-__device__ __forceinline__ void lay_out_x(const X16& v, bool on, bool slot, __half* dst, int half, float* xs, int t4) {
+// a power of two of the block's own, which it returns the inverse of: bf16 has
+// 8 significant bits and fp16 11, and the power of two puts the largest finite
+// value into [2^14, 2^15): a value down to 2^-31 of the largest is kept exactly,
+// a smaller one to half of fp16's last step 2^-24, 2^-39 of the largest, below
+// what an fp32 sum keeps.  Infinities and NaN stay what they are.
+__device__ __forceinline__ float half_x(const X16& v, uint32_t (&h)[8]) {
     uint32_t top = 0;
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -137,24 +146,22 @@ __device__ __forceinline__ void lay_out_x(const X16& v, bool on, bool slot, __ha
     // 2^(14 - e) for the largest value's exponent e, kept within what fp32 holds as a normal number
     const int e = min(max((int)(top >> 7) - 127, -112), 127);
     const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-    uint32_t h[8];
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t w = v.w(i);
         const __half2 p = __floats2half2_rn(bf16_f(w & 0xffffu) * up, __uint_as_float(w & 0xffff0000u) * up);
         h[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    if (on) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(dst + half) = make_uint4(h[4], h[5], h[6], h[7]);
-    }
-    if (slot && t4 == 0) *xs = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+    return __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }
 
 // u = x A^T for 16 rows of A (blockIdx.y) of one projection (blockIdx.z), the
 // blocks of 64 along K shared out over the cluster's CTAs and their warps,
 // and x laid out for lsn_decode_kernel.  Sums in fp32: MMA accumulators, then
-// the warps in order, then the cluster's CTAs in order.
+// the warps in order, then the cluster's CTAs in order, then (add_adapter)
+// the slices.  Bound by latency: one round of loads for each warp, which is
+// why rows of more than 128 blocks take more clusters (72B down, 8 tokens:
+// 59.0 us with one, 57.1 with four).
 template <int TP>
 __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __grid_constant__ PrepArgs args) {
     constexpr int NT = (TP + 7) / 8;
@@ -197,7 +204,14 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
                 for (int i = 0; i < NT; ++i) {
                     const int t = g + 8 * i;
                     // absent tokens (all zeros) take part in the shuffles and leave a scale that multiplies zeros
-                    lay_out_x(xv[i], t < T, t < TP, p.xf + ((int64_t)b * 2 * TP + t) * 32 + 8 * t4, TP * 32, p.xs + (int64_t)b * TP + t, t4);
+                    uint32_t h[8];
+                    const float scale = half_x(xv[i], h);
+                    if (t < T) {
+                        __half* const d = p.xf + ((int64_t)b * 2 * TP + t) * 32 + 8 * t4;
+                        *reinterpret_cast<uint4*>(d) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(d + TP * 32) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                    if (t < TP && t4 == 0) p.xs[(int64_t)b * TP + t] = scale;
                 }
             }
         }
@@ -371,18 +385,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ float ldsf(uint32_t a) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ void stsf(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-
 __device__ __forceinline__ void stsf4(uint32_t a, float4 v) {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
@@ -470,9 +478,14 @@ __device__ __forceinline__ void add_adapter(const DecodeArgs& a, const DecodePro
 // projections.  Each warp streams its own stages (32 rows x 128 bytes) through
 // a ring of TMA copies, looks every pair of codes up in the table and
 // multiplies on the tensor cores; nothing is shared between the warps until a
-// tile's sums are complete.  A tile
-// cut between CTAs is added up by the CTA that finishes it last, in the order
-// of the CTAs.
+// tile's sums are complete.  A tile cut between CTAs is added up by the CTA
+// that finishes it last, in the order of the CTAs.
+//
+// Bound by instruction issue and the table's loads, with about 10 us of launch,
+// preparation and joins: 8B layer in a CUDA graph (floor 17.8 us), one token
+// 40.4 us, 8 tokens 50.1, 16 tokens 66.0; 72B down, 8 tokens 57.6 us (floor
+// 19.6).  Stages shared by the CTA, filled and scaled by producer warps, took
+// 48-55 us where this took 46 (the absmax values of 512 rows kept them behind).
 //
 // TP is the padded token count.  8 or 16: the MMA's columns are tokens, and
 // each block of 64 is scaled by its absmax after its four MMAs.  2: a column
@@ -808,29 +821,6 @@ constexpr int kAhead = 2;               // blocks of a warp whose codes are in f
 template <int NT>
 constexpr int small_smem(int groups) {  // table, partial sums of y and, for each 16 ranks, of u
     return 65536 + kWarps * kRows * 8 * NT * 4 + groups * kWarps * 16 * 8 * NT * 4;
-}
-
-// The fp16 form of 16 of a token's 64 values (one lane of a quad) and its scale, as lay_out_x stores them.
-__device__ __forceinline__ float half_x(const X16& v, uint32_t (&h)[8]) {
-    uint32_t top = 0;
-    #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t w = v.w(i) & 0x7fff7fffu;
-        const uint32_t lo = w & 0xffffu, hi = w >> 16;
-        if (lo < 0x7f80u) top = max(top, lo);
-        if (hi < 0x7f80u) top = max(top, hi);
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = min(max((int)(top >> 7) - 127, -112), 127);
-    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-    #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t w = v.w(i);
-        const __half2 p = __floats2half2_rn(bf16_f(w & 0xffffu) * up, __uint_as_float(w & 0xffff0000u) * up);
-        h[i] = *reinterpret_cast<const uint32_t*>(&p);
-    }
-    return __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }
 
 template <int NT>

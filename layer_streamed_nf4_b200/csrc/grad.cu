@@ -116,6 +116,7 @@ __device__ double block_sum(double v, double* sh) {
     return v;               // the sum, in thread 0
 }
 
+// Bound by reading (168 MB).
 // Partial sums of one launch's tensors; with `last`, the last CTA to finish
 // adds those of every launch (`parts` in all, in order) and writes the norm.
 template <int MAX>
@@ -174,7 +175,9 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_norm_kernel(const __grid_co
     }
 }
 
-// The last chunks first: they are what the norm read last and the L2 still holds.
+// The last chunks first: they are what the norm read last and the L2 still
+// holds.  Bound by reading and writing: norm and scaling of 168 MB take 80 us
+// together, 78 at the copy rate.
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_constant__ GradArgs<MAX> a, const GradWs* ws) {
     pdl_wait();
