@@ -272,7 +272,10 @@ __device__ __forceinline__ void pair_loss(const Finish& f, double h, double* los
 // each: the rows' pieces joined into lse, the sequences' sums in fp64 (hundreds
 // of terms that later cancel against the reference's), the loss, its gradients
 // and, for the gradient kernel of the same call, every row's factor; the last
-// CTA to finish adds the losses up in order.  Bound by its chain of loads.
+// CTA to finish adds the losses up in order.  Bound by its chain of loads, of
+// which those of the caller's tensors come before pdl_wait: the statistics
+// kernel does not write them and itself began after everything older was
+// complete (without it, T = 0, they wait like the rest).
 __global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __grid_constant__ Rows r, const __grid_constant__ Finish f) {
     constexpr int kHalf = kFinThreads / 2;
     __shared__ double sums[kFinThreads / 32];
@@ -280,19 +283,20 @@ __global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __gri
     __shared__ double lp[2];
     __shared__ float c_row[2];
     __shared__ int is_last;
-    pdl_wait();
-    pdl_launch_dependents();
+    if (r.T == 0) pdl_wait();
     const int half = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, warp = threadIdx.x >> 5;
     const int q = 2 * blockIdx.x + half;
     const bool have = q < r.n_seq;
     const int a = have ? max(r.start[q], 0) : 0, b = have ? min(r.start[q + 1], r.T) : 0;
     const double ref0 = f.ref ? f.ref[2 * blockIdx.x] : 0.0, ref1 = f.ref ? f.ref[2 * blockIdx.x + 1] : 0.0;     // (pairs only)
+    const bool on0 = a + tid < b && scored(r, a + tid, r.targets[a + tid]);
+    if (r.T > 0) pdl_wait();
+    pdl_launch_dependents();
     double sum = 0.0;
     int n = 0;
     for (int t = a + tid; t < b; t += kHalf) {
-        const int y = r.targets[t];
         float l = 0.f;
-        if (scored(r, t, y)) {
+        if (t == a + tid ? on0 : scored(r, t, r.targets[t])) {
             float m = -INFINITY, s = 0.f;
             #pragma unroll 4
             for (int i = 0; i < r.splits; ++i) {
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __gri
     if (f.coef) {
         float c = c_row[half];
         if (r.average) c /= (float)counts[half * (kHalf / 32)];
-        for (int t = a + tid; t < b; t += kHalf) f.coef[t] = scored(r, t, r.targets[t]) ? c : 0.f;
+        for (int t = a + tid; t < b; t += kHalf) f.coef[t] = (t == a + tid ? on0 : scored(r, t, r.targets[t])) ? c : 0.f;
     }
     if (f.mean == nullptr) return;
     __syncthreads();
@@ -423,19 +427,30 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) 
 // whole loss).  Bound by reading the logits and writing their gradient: 171 us
 // there, 6.4 TB/s.  Where a row of logits and its row of gradients lie
 // differently against 16 bytes, words are put together from two neighbours.
+// Behind the finishing kernel (coef) the first logits are asked for before
+// pdl_wait, into the L2 (into registers the kernel's loop came out slower: 274
+// us where this takes 255).
 template <class E>
 __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_constant__ Rows r, const float* lse, const float* dlogp,
                                                                 const int32_t* count, const float* coef, E* dl, int64_t ld_d) {
     constexpr int per = Words<E>::per;
     constexpr int U = 4;
-    pdl_wait();
-    pdl_launch_dependents();
+    if (coef == nullptr) pdl_wait();
     const unsigned item = gridDim.x - 1 - blockIdx.x;
     const int t = (int)(item / (unsigned)r.splits), split = (int)(item % (unsigned)r.splits);
     const int y = r.targets[t];
     const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
     E* out = dl + (int64_t)t * ld_d;
     const bool on = scored(r, t, y);
+    const int o = (int)((reinterpret_cast<uintptr_t>(row) - reinterpret_cast<uintptr_t>(out)) & 15);   // 0: they lie alike
+    const Piece p = piece_of<E>(out, r.V, split, r.splits, o ? 1 : 0);
+    // with the out row's words: word w's elements start o bytes into word w of `words`
+    const uint4* words = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row - p.mis) & ~(uintptr_t)15);
+    uint4* outs = reinterpret_cast<uint4*>(out - p.mis);
+    if (on && threadIdx.x < U * kThreads / 8 && p.w0 + 8 * (int)threadIdx.x < p.w1)      // a line each
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(words + p.w0 + 8 * threadIdx.x));
+    if (coef != nullptr) pdl_wait();
+    pdl_launch_dependents();
     float c = 0.f;
     if (on) {
         if (coef != nullptr) {
@@ -447,11 +462,6 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_con
         }
     }
     const float nc = -c, L = on ? lse[t] : 0.f;
-    const int o = (int)((reinterpret_cast<uintptr_t>(row) - reinterpret_cast<uintptr_t>(out)) & 15);   // 0: they lie alike
-    const Piece p = piece_of<E>(out, r.V, split, r.splits, o ? 1 : 0);
-    // with the out row's words: word w's elements start o bytes into word w of `words`
-    const uint4* words = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row - p.mis) & ~(uintptr_t)15);
-    uint4* outs = reinterpret_cast<uint4*>(out - p.mis);
     if (!on) {
         for (int w = p.w0 + threadIdx.x; w < p.w1; w += kThreads) __stcs(&outs[w], make_uint4(0, 0, 0, 0));
     } else {
