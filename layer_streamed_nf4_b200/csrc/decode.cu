@@ -107,6 +107,9 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Has the line at p brought into the L2.
+__device__ __forceinline__ void l2_hint(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ float bf16_f(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
 
 // The four registers of 16 consecutive bf16 (32 bytes) split over two 16-byte loads.
@@ -170,6 +173,13 @@ __global__ void __launch_bounds__(kPrepThreads) lsn_decode_prep_kernel(const __g
     const int slice = blockIdx.x / kPrepCtas, slices = args.p[blockIdx.z].slices;
     const bool dots = args.p[blockIdx.z].A != nullptr && slice < slices;       // the same for the whole cluster
     if (dots) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");    // started: waited for before writing to CTA 0
+    {   // a warp's first block of A, into the L2: a hint that reads nothing, so it need not wait (0.5B layer, one
+        // token, after such a call: 13.3 -> 12.4 us)
+        const PrepProj& p = args.p[blockIdx.z];
+        const int lane = threadIdx.x & 31, b = blockIdx.x * kPrepWarps + (threadIdx.x >> 5), j = blockIdx.y * 16 + lane;
+        if (dots && lane < 16 && j < args.r && b < p.nb)
+            l2_hint(p.A + (int64_t)j * p.nb * 64 + (int64_t)b * 64);
+    }
     pdl_wait();
     pdl_launch_dependents();
     for (int i = ((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * kPrepThreads + threadIdx.x; i < args.n_counters;
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
         const float offset = *p.offset;
         float acc[2][NT][4] = {};
         if (p.u != nullptr && mine)             // read at the tile's end
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.B + (int64_t)(rg * kRows + lane) * args.r));
+            l2_hint(p.B + (int64_t)(rg * kRows + lane) * args.r);
         const char* const xf = reinterpret_cast<const char*>(p.xf) + (TP == 2 ? (g >> 1) * (TP * 128) + (g & 1) * 64 : g * 64) + t4 * 16;
         const char* const xsp = reinterpret_cast<const char*>(p.xs) + t4 * 8;
         for (int n = cur.here; n > 0; --n) {
@@ -782,9 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
 
 // Taken while its rounds (CTAs over SMs, times 1024 codes of a row at a time)
 // are few.  Measured in a graph, this launch against the two: 512 x 512, one
-// token, 2.8 and 8.0 us; 4096 x 1024, 16 tokens, 7.6 and 14.9; 4096 x 4096, one
-// token, 9.7 and 10.9 (rank 64: 14.0 and 12.9); 8192 x 2048, 8 tokens, 12.7
-// and 12.0; the seven 0.5B projections, one token, 18.6 and 14.2.
+// token, 2.7 and 8.0 us; 4096 x 1024, 16 tokens, 7.2 and 14.9; 4096 x 4096, one
+// token, 9.0 and 10.9 (rank 64: 14.0 and 12.3); 8192 x 2048, 8 tokens, 12.2
+// and 12.0; the seven 0.5B projections, one token, 18.6 and 12.4.
 constexpr int64_t kSmallRounds = 4;
 
 // absmax = offset + table[q] s2 with table[q] = (q - 127) / 127, [255] = 0
@@ -844,6 +854,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) lsn_decode_small_kernel(cons
             *reinterpret_cast<__half2*>(smem_raw + (warp * 16 + i) * 256 + lane * 4) = h;
         }
     }
+    // the tile's codes, into the L2: hints that read nothing, so they need not wait (9.7 -> 9.0 us)
+    for (int64_t i = (int64_t)threadIdx.x * 128; i < (int64_t)kRows * nb * 32; i += kSmallThreads * 128)
+        l2_hint(p.packed + (int64_t)n0 * nb * 32 + i);
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
