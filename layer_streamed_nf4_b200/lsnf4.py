@@ -242,6 +242,18 @@ def _dev(t, rows: bool = False) -> int | None:
     return t.data_ptr()
 
 
+def _devs(*tensors) -> list:
+    """The device addresses of several tensors: _dev of each, with the current device asked for once."""
+    here, out = None, []
+    for t in tensors:
+        if t is not None and type(t) is not int:
+            if here is None:
+                here = _current_device()
+            t = t.data_ptr() if t.get_device() == here and t.is_contiguous() else _dev(t)
+        out.append(t)
+    return out
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return _current_stream()
@@ -383,8 +395,9 @@ def decode_ws_bytes(projs, T: int, r: int) -> int:
 def lora_linear_decode(W: Base, x, T: int, A, B, r: int, scale: float, y, ws, ws_bytes: int, stream=None):
     """y = x W^T + scale (x A^T) B^T for T <= LSN_DECODE_MAX_T tokens, W an NF4 base read from its codes (A and B
     None: adapter off)."""
-    _check(_lib.lora_linear_decode(ctypes.byref(W), _dev(x), T, _dev(A), _dev(B), r, scale, _dev(y), _dev(ws),
-                                   ws_bytes, _stream(stream)), "lora_linear_decode")
+    x, A, B, y, ws = _devs(x, A, B, y, ws)
+    _check(_lib.lora_linear_decode(ctypes.byref(W), x, T, A, B, r, scale, y, ws, ws_bytes, _stream(stream)),
+           "lora_linear_decode")
 
 
 def lora_layer_decode(projs, T: int, r: int, scale: float, ws, ws_bytes: int, stream=None):
@@ -412,28 +425,28 @@ def seq_logp_ws_bytes(sl: SeqLogits) -> int:
 
 def seq_logp_fwd(sl: SeqLogits, lse, logp, count, ws, ws_bytes: int, stream=None):
     """lse fp32 [T], logp fp64 [n_seq] and (or None) count int32 [n_seq] of a batch of sequences."""
-    _check(_lib.seq_logp_fwd(ctypes.byref(sl), _dev(lse), _dev(logp), _dev(count), _dev(ws), ws_bytes,
-                             _stream(stream)), "seq_logp_fwd")
+    lse, logp, count, ws = _devs(lse, logp, count, ws)
+    _check(_lib.seq_logp_fwd(ctypes.byref(sl), lse, logp, count, ws, ws_bytes, _stream(stream)), "seq_logp_fwd")
 
 
 def seq_logp_bwd(sl: SeqLogits, lse, dlogp, count, dlogits, ld_d: int, stream=None):
-    _check(_lib.seq_logp_bwd(ctypes.byref(sl), _dev(lse), _dev(dlogp), _dev(count), _dev(dlogits), ld_d,
-                             _stream(stream)), "seq_logp_bwd")
+    lse, dlogp, count = _devs(lse, dlogp, count)
+    _check(_lib.seq_logp_bwd(ctypes.byref(sl), lse, dlogp, count, _dev(dlogits, rows=True), ld_d, _stream(stream)),
+           "seq_logp_bwd")
 
 
 def preference_loss_fwd(sl: SeqLogits, ref_logp, p: Preference, lse, logp, count, reward, loss, mean_loss, dlogp, ws,
                         ws_bytes: int, stream=None):
-    _check(_lib.preference_loss_fwd(ctypes.byref(sl), _dev(ref_logp), ctypes.byref(p), _dev(lse), _dev(logp),
-                                    _dev(count), _dev(reward), _dev(loss), _dev(mean_loss), _dev(dlogp), _dev(ws),
-                                    ws_bytes, _stream(stream)), "preference_loss_fwd")
+    ref_logp, *out, ws = _devs(ref_logp, lse, logp, count, reward, loss, mean_loss, dlogp, ws)
+    _check(_lib.preference_loss_fwd(ctypes.byref(sl), ref_logp, ctypes.byref(p), *out, ws, ws_bytes, _stream(stream)),
+           "preference_loss_fwd")
 
 
 def preference_loss_fwd_bwd(sl: SeqLogits, ref_logp, p: Preference, lse, logp, count, reward, loss, mean_loss, dlogp,
                             dlogits, ld_d: int, ws, ws_bytes: int, stream=None):
-    _check(_lib.preference_loss_fwd_bwd(ctypes.byref(sl), _dev(ref_logp), ctypes.byref(p), _dev(lse), _dev(logp),
-                                        _dev(count), _dev(reward), _dev(loss), _dev(mean_loss), _dev(dlogp),
-                                        _dev(dlogits), ld_d, _dev(ws), ws_bytes, _stream(stream)),
-           "preference_loss_fwd_bwd")
+    ref_logp, *out, ws = _devs(ref_logp, lse, logp, count, reward, loss, mean_loss, dlogp, ws)
+    _check(_lib.preference_loss_fwd_bwd(ctypes.byref(sl), ref_logp, ctypes.byref(p), *out, _dev(dlogits, rows=True),
+                                        ld_d, ws, ws_bytes, _stream(stream)), "preference_loss_fwd_bwd")
 
 
 # -------------------------------------------- gradient norm and clipping ---
@@ -457,12 +470,14 @@ def grad_ws_bytes(tensors) -> int:
 
 def grad_norm(tensors, norm, ws, ws_bytes: int, stream=None):
     arr = _grads(tensors)
-    _check(_lib.grad_norm(len(arr), arr, _dev(norm), _dev(ws), ws_bytes, _stream(stream)), "grad_norm")
+    norm, ws = _devs(norm, ws)
+    _check(_lib.grad_norm(len(arr), arr, norm, ws, ws_bytes, _stream(stream)), "grad_norm")
 
 
 def grad_clip(tensors, max_norm: float, norm, ws, ws_bytes: int, stream=None):
     arr = _grads(tensors)
-    _check(_lib.grad_clip(len(arr), arr, max_norm, _dev(norm), _dev(ws), ws_bytes, _stream(stream)), "grad_clip")
+    norm, ws = _devs(norm, ws)
+    _check(_lib.grad_clip(len(arr), arr, max_norm, norm, ws, ws_bytes, _stream(stream)), "grad_clip")
 
 
 def selftest_wait_timeout(limit_us: int = 1000, stream=None) -> int:

@@ -202,6 +202,22 @@ def test_in_place_gradients(lib, dtype, V, pad, offset):
     assert torch.equal(b.logits[:, V:], behind)
 
 
+def test_tensors_that_are_columns_of_wider_ones(lib):
+    import torch
+    b = Batch(lib, (9, 14, 3, 2), 501, 11, seed=6)
+    p = lib.preference(lib.LSN_PREF_SIGMOID, 0.3)
+    want, wide = (torch.full((b.T, n), 7.0, dtype=b.dt, device="cuda") for n in (b.V, b.V + 20))
+    a = b.refd, p, b.lse, b.logp, b.count, b.reward, b.loss, b.mean, b.dlogp
+    lib.preference_loss_fwd_bwd(b.sl, *a, want, b.V, b.ws, b.nws)
+    sl = lib.seq_logits(b.logits[:, :b.V], b.T, b.V, b.ld, lib.LSN_DT_BF16, b.tgt, b.n, b.st)
+    lib.preference_loss_fwd_bwd(sl, *a, wide[:, 8:8 + b.V], b.V + 20, b.ws, b.nws)
+    assert torch.equal(wide[:, 8:8 + b.V], want) and bool((wide[:, :8] == 7).all()) and bool((wide[:, 8 + b.V:] == 7).all())
+    lib.seq_logp_bwd(sl, b.lse, b.dlogp, b.count, wide[:, 3:3 + b.V], b.V + 20)
+    assert torch.equal(wide[:, 3:3 + b.V], want)
+    with pytest.raises(lib.LsnError, match="strides"):
+        lib.seq_logp_bwd(sl, b.lse, b.dlogp, b.count, torch.zeros(b.V, b.T, dtype=b.dt, device="cuda").t(), b.T)
+
+
 @pytest.mark.parametrize("kind", [0, 1, 2])
 def test_without_a_reference_and_optional_outputs(lib, kind):
     import torch
