@@ -493,8 +493,8 @@ __device__ __forceinline__ void add_adapter(const DecodeArgs& a, const DecodePro
 //
 // Bound by instruction issue and the table's loads, with about 10 us of launch,
 // preparation and joins: 8B layer in a CUDA graph (floor 17.8 us), one token
-// 40.4 us, 8 tokens 50.1, 16 tokens 66.0; 72B down, 8 tokens 57.6 us (floor
-// 19.6).  Stages shared by the CTA, filled and scaled by producer warps, took
+// 40.0 us, 8 tokens 49.2, 16 tokens 66.5; 72B down, 8 tokens 57 to 64 us by
+// machine (floor 19.6).  Stages shared by the CTA, filled and scaled by producer warps, took
 // 48-55 us where this took 46 (the absmax values of 512 rows kept them behind).
 //
 // TP is the padded token count.  8 or 16: the MMA's columns are tokens, and
