@@ -64,6 +64,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSmallMax = 1e38f;         // maxima below it: one multiply-add a logit
 
 template <class E> struct Words;           // 16-byte words of a row: how many values, and unpacking
 template <> struct Words<uint16_t> {
@@ -171,18 +172,19 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
     const E* row = reinterpret_cast<const E*>(r.logits) + (int64_t)t * r.ld;
     const Piece p = piece_of<E>(row, r.V, split, r.splits, 0);
     const uint4* words = reinterpret_cast<const uint4*>(row - p.mis);
-    float m = -INFINITY, c = -INFINITY, s = 0.f;        // s: the sum of exp2(x log2 e - c), c about m log2 e
+    // s: the sum of exp2(x log2 e - c), c about m log2 e, for a small m; of exp2((x - m) log2 e) for a large one
+    float m = -INFINITY, c = -INFINITY, s = 0.f;
     for (int w = p.w0 + threadIdx.x; w < p.w1; w += U * kThreads) {
         uint4 x[U];
         #pragma unroll
         for (int u = 0; u < U; ++u) x[u] = w + u * kThreads < p.w1 ? words[w + u * kThreads] : Words<E>::none();
         const int first = w - (int)(threadIdx.x & 31);      // of the warp's words; those past the end are -infinity
-        const float top = fmaxf(m, Words<E>::template largest<U>(x));
+        const float old = m, top = fmaxf(m, Words<E>::template largest<U>(x));
         m = top;
-        if (fabsf(top) < 1e38f) {
+        if (fabsf(top) < kSmallMax) {
             // c is a number like any other: what its rounding leaves out is put right at the end
             const float c1 = top * kLog2e;
-            if (c1 != c) s *= ex2(c - c1);
+            if (c1 != c) s *= ex2(fabsf(old) < kSmallMax ? c - c1 : fmaf(old, kLog2e, -c1));
             c = c1;
             #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
             }
         } else {                                        // the type's lowest value, infinities, nothing yet
             const float at = top == -INFINITY ? 0.f : top;
-            c = top * kLog2e;
+            if (top != old) s *= ex2(fabsf(old) < kSmallMax ? -fmaf(at, kLog2e, -c) : (old - at) * kLog2e);
             #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float v[per];
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
             }
         }
     }
-    if (fabsf(m) < 1e38f) s *= ex2(-fmaf(m, kLog2e, -c));
+    if (fabsf(m) < kSmallMax) s *= ex2(-fmaf(m, kLog2e, -c));
     if (split == 0) {
         if (threadIdx.x == 0) ly[t] = Words<E>::one(row + y);
         const int edge = p.head + r.V - p.tail;

@@ -439,3 +439,24 @@ def test_offsets_beyond_32_bits(lib):
     want[torch.arange(64, device="cuda"), tgt[-64:].long()] += 2.0
     assert float((logits[-64:].double() - want).abs().max()) <= 2.0 * 2.0 ** -8
     assert float((logits[0].float() + 1.0 / V).abs().median()) <= 2.0 ** -8 / V
+
+
+@pytest.mark.parametrize("dtype,T,V", [("bf16", 1200, 12000), ("fp32", 300, 8190)])
+@pytest.mark.parametrize("first,later", [(-3.3e38, -2e38), (1.5e38, 3e38), (0.5, 2e38), (-1e5, -7e4), (6e4, 7e4), (-7e4, -6e4)])
+def test_a_maximum_that_grows_along_the_row(lib, dtype, T, V, first, later):
+    """One piece of a row, two rounds of each thread: the first 4 x 256 words hold one value, the rest a larger one,
+    over which the row is uniform."""
+    import torch
+    b = Batch(lib, (9, 7), V, dtype=dtype, tail=T - 16, seed=1, prompt=0.0)
+    n = 1024 * (8 if dtype == "bf16" else 4)
+    b.logits[:16, :n] = first
+    b.logits[:16, n:V] = later
+    b.targets[:16] = np.random.default_rng(0).integers(n, V, 16)
+    b.targets[16:] = -100
+    b.upload()
+    lib.seq_logp_fwd(b.sl, b.lse, b.logp, b.count, b.ws, b.nws)
+    torch.cuda.synchronize()
+    ts = b.tol_s(np.zeros(1))
+    want, m = -np.log(V - n), float(b.logits[0, V - 1])
+    assert (np.abs(b.logp.cpu().numpy() - want * np.array([9, 7])) <= np.array([9, 7]) * ts).all(), (b.logp, want)
+    assert (np.abs(b.lse[:16].double().cpu().numpy() - (m - want)) <= ts + abs(m) * 2.0 ** -24).all()
