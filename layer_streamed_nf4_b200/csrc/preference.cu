@@ -64,7 +64,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSmallMax = 1e38f;         // maxima below it: one multiply-add a logit
+// Maxima below it take one multiply-add a logit: the rounding of their product with
+// log2 e, which is left in the sum until the end, is at most 2^-8 there.  (From 2^31
+// on it leaves exp2's range.)
+constexpr float kSmallMax = 65536.f;
 
 template <class E> struct Words;           // 16-byte words of a row: how many values, and unpacking
 template <> struct Words<uint16_t> {
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
                 #pragma unroll
                 for (int i = 0; i < per; ++i) s += ex2(fmaf(v[i], kLog2e, -c1));
             }
-        } else {                                        // the type's lowest value, infinities, nothing yet
+        } else {                                        // masks of any size, infinities, nothing yet
             const float at = top == -INFINITY ? 0.f : top;
             if (top != old) s *= ex2(fabsf(old) < kSmallMax ? -fmaf(at, kLog2e, -c) : (old - at) * kLog2e);
             #pragma unroll

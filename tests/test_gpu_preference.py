@@ -460,3 +460,89 @@ def test_a_maximum_that_grows_along_the_row(lib, dtype, T, V, first, later):
     want, m = -np.log(V - n), float(b.logits[0, V - 1])
     assert (np.abs(b.logp.cpu().numpy() - want * np.array([9, 7])) <= np.array([9, 7]) * ts).all(), (b.logp, want)
     assert (np.abs(b.lse[:16].double().cpu().numpy() - (m - want)) <= ts + abs(m) * 2.0 ** -24).all()
+
+
+def check_scored_rows(lib, b, beta=0.1):
+    """The whole loss with its gradient against fp64 on the scored rows, with the tolerances of the checks above."""
+    import torch
+    d = torch.full((b.T, b.V), 9.0, dtype=b.dt, device="cuda")
+    p = lib.preference(lib.LSN_PREF_SIGMOID, beta)
+    lib.preference_loss_fwd_bwd(b.sl, b.refd, p, b.lse, b.logp, b.count, b.reward, b.loss, b.mean, b.dlogp, d, b.V, b.ws, b.nws)
+    torch.cuda.synchronize()
+    rows = np.flatnonzero((b.targets >= 0) & (b.targets < b.V) & (np.arange(b.T) >= b.start[0]) & (np.arange(b.T) < b.start[-1]))
+    x = b.logits[torch.from_numpy(rows).cuda(), :b.V].double()
+    tgt = torch.from_numpy(b.targets[rows]).long().cuda()
+    lse = torch.logsumexp(x, 1)
+    near = x[x > x.amax(1, keepdim=True) - 200]
+    ts = b.tol_s(np.array([float(near.min()), float(near.max())]))
+    assert bool(((b.lse[torch.from_numpy(rows).cuda()].double() - lse).abs() <= ts + lse.abs() * 2.0 ** -24).all())
+    tok = (x.gather(1, tgt[:, None])[:, 0] - lse).cpu().numpy()
+    seq = np.searchsorted(b.start, rows, side="right") - 1
+    logp, n = np.bincount(seq, tok, b.n), np.bincount(seq, minlength=b.n)
+    assert (np.abs(b.logp.cpu().numpy() - logp) <= n * ts + 1e-12 * np.abs(logp)).all()
+    a, err = logp - b.ref, n * ts + 1e-12 * np.abs(logp)
+    h, dh = a[0::2] - a[1::2], err[0::2] + err[1::2]
+    loss, dl, curv = loss64(0, beta, 0.0, h)
+    assert (np.abs(b.loss.cpu().numpy() - loss) <= np.abs(dl) * dh + curv * dh ** 2 + np.abs(loss) * 2.0 ** -23 + 1e-30).all()
+    c = np.stack([dl, -dl], 1).reshape(-1) / len(h)
+    dc = np.repeat(curv * dh, 2) / len(h) + np.abs(c) * 2.0 ** -23
+    C, dC = (torch.from_numpy(v[seq]).cuda()[:, None] for v in (np.abs(c), dc))
+    arg = x - lse[:, None]
+    prob, hot = arg.exp(), torch.zeros_like(x).scatter_(1, tgt[:, None], 1.0)
+    want = torch.from_numpy(c[seq]).cuda()[:, None] * (hot - prob)
+    rel = ts + lse.abs()[:, None] * 2.0 ** -24 + 2.0 ** -22 + 2 * arg.abs().clamp_max(200) * 1.45 * 2.0 ** -24
+    half = 2.0 ** -8 if b.dt == torch.bfloat16 else 2.0 ** -24
+    tol = C * prob * rel + dC * (hot - prob).abs() + C * (hot + prob) * 2.0 ** -23 + want.abs() * half + 1e-37
+    bad = ~((d[torch.from_numpy(rows).cuda()].double() - want).abs() <= tol)
+    assert not bool(bad.any()), int(bad.sum())
+    off = torch.ones(b.T, dtype=torch.bool, device="cuda")
+    off[torch.from_numpy(rows).cuda()] = False
+    assert bool((d[off] == 0).all())
+
+
+MASKS = [(-1e4,), (-66000.0, -65000.0), (-1e5,), (-1e9,), (-2e9,), (-3e9,), (-1e10,), (-1e20,), (-1e30,), (-3e37,), (-1e10, -1e30),
+         (float("-inf"), -1e12, -3.3e38)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("masks", MASKS, ids=str)
+@pytest.mark.parametrize("where", ["words", "all but a few", "halves"])
+@pytest.mark.parametrize("lens,V,tail", [((6, 8, 5, 3), 700, 0), ((6, 8), 32003, 2), ((6, 8), 12000, 1190)])
+def test_finite_masks_of_any_size(lib, lens, V, tail, where, masks, dtype):
+    """Tokens masked with a finite number take no probability, whatever its size, and leave the other tokens theirs:
+    single aligned words, whole rows but a few tokens, the first half of a row; rows of one word a thread and of
+    several."""
+    b = Batch(lib, lens, V, dtype=dtype, tail=tail, seed=3, prompt=0.2)
+    rng = np.random.default_rng(1)
+    word = 16 // b.logits.element_size()
+    for t in range(int(b.start[-1])):
+        m = masks[t % len(masks)] if t % 3 else masks[0]
+        keep = np.unique(np.append(rng.integers(0, V, 5), b.targets[t] if 0 <= b.targets[t] < V else 0))
+        old = b.logits[t, keep].clone()
+        if where == "words":
+            for w in rng.integers(0, V // word, 6):
+                b.logits[t, w * word:(w + 1) * word] = m
+        elif where == "halves":
+            b.logits[t, :V // 2] = m
+        else:
+            b.logits[t] = m
+            if len(masks) > 1:
+                b.logits[t, V // 3:2 * V // 3] = masks[(t + 1) % len(masks)]
+        b.logits[t, keep] = old
+    check_scored_rows(lib, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("top", [7e4, 3e9, 1e10, 1e30])
+def test_one_large_logit(lib, top, dtype):
+    """A token far above the others has probability one."""
+    import torch
+    b = Batch(lib, (6, 8), 700, dtype=dtype, seed=4, prompt=0.0)
+    at = np.random.default_rng(2).integers(0, 700, b.T)
+    b.logits[torch.arange(b.T, device="cuda"), torch.from_numpy(at).cuda()] = top
+    b.targets[:] = at
+    b.upload()
+    d = torch.empty(b.T, b.V, dtype=b.dt, device="cuda")
+    lib.preference_loss_fwd_bwd(b.sl, None, lib.preference(0, 0.1), b.lse, b.logp, b.count, b.reward, b.loss, b.mean, b.dlogp, d, b.V, b.ws, b.nws)
+    torch.cuda.synchronize()
+    assert bool((b.lse[:b.T] == b.logits[0, at[0]].float()).all()) and bool((b.logp == 0).all()) and bool((d == 0).all())
