@@ -82,7 +82,9 @@ the same numerics):
 """
 from __future__ import annotations
 
+import copy
 import ctypes
+import weakref
 from dataclasses import dataclass
 
 import torch
@@ -287,12 +289,19 @@ class Stack:
                 lsnf4.layer_pool_prefetch(self.pool, l)
             lsnf4.layer_pool_wait_idle(self.pool, 600000)
 
+    def _copy(self) -> "Stack":
+        """This stack's state, less what belongs to it alone: the losses and the few-token workspace that its
+        check_status() asks for."""
+        other = copy.copy(self)
+        other._preferences = ()
+        other._decode_ws = other._decode_ws_T = None
+        return other
+
     def with_mode(self, mode: str, n_slots: int = 2, lanes: int | None = None, api: str | None = None) -> "Stack":
         """A stack sharing this one's host blobs and tensors, run in another mode
         (and, if given, another lane count)."""
-        import copy
         assert mode in ("resident", "streamed", "no_h2d")
-        other = copy.copy(self)
+        other = self._copy()
         other.mode, other.pool, other.resident, other._calls = mode, None, None, {}
         other.ahead = other._ahead_for(mode)
         if api is not None and api != self.api:
@@ -319,8 +328,7 @@ class Stack:
     def with_tokens(self, tokens: int, mode: str = "streamed", n_slots: int = 2) -> "Stack":
         """A stack sharing this one's host blobs (the frozen base) and adapters' seeds, with its own
         activations for `tokens` tokens (a larger batch streams the same weights)."""
-        import copy
-        other = copy.copy(self)
+        other = self._copy()
         other.T, other.mode = tokens, mode
         other.pool, other.resident, other._calls = None, None, {}
         other.ahead = other._ahead_for(mode)
@@ -448,8 +456,7 @@ class Stack:
                     n_slots: int = 2) -> "Stack":
         """A stack sharing this one's host blobs, with its own activations: shared inputs per group of
         projections, and (grouped) the groups passed to the layer calls."""
-        import copy
-        other = copy.copy(self)
+        other = self._copy()
         other.shared_inputs, other.grouped = shared_inputs or grouped, grouped
         other.mode, other.pool, other.resident, other._calls = mode, None, None, {}
         other.ahead = other._ahead_for(mode)
@@ -690,8 +697,16 @@ class Stack:
         return lsnf4.layer_pool_stats(self.pool) if self.pool is not None else None
 
     def check_status(self):
+        """Raises if a kernel gave up on a bounded wait since the last check: in the sweeps, in decode(), or in the
+        head of a Preference of this stack."""
         for ws, ln in zip(self.ws, self.lanes):
             lsnf4.ws_status(ws, ln)
+        if getattr(self, "_decode_ws", None) is not None:
+            lsnf4.ws_status(self._decode_ws, self.stream)
+        for ref in getattr(self, "_preferences", ()):
+            pr = ref()
+            if pr is not None:
+                pr.check_status()
 
 
 class Preference:
@@ -741,6 +756,16 @@ class Preference:
         self._ws_bytes = lsnf4.seq_logp_ws_bytes(self._in)
         self._ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=dev)
         torch.cuda.synchronize(dev)
+        self._register()
+
+    def _register(self):
+        """The stack's check_status() asks for this loss's head too, while it lives."""
+        alive = [p for p in getattr(self.stack, "_preferences", ()) if p() is not None]
+        self.stack._preferences = [*alive, weakref.ref(self)]
+
+    def check_status(self):
+        """Raises if a kernel of the head gave up on a bounded wait since the last check."""
+        lsnf4.ws_status(self._hws, self.stack.stream)
 
     def run(self):
         """After the stack's forward(reference=True): the loss, and its gradient in the stack's last dY."""

@@ -176,3 +176,21 @@ def test_the_three_together(lib):
     assert any(not torch.equal(few.y[0, i], before[i]) for i in range(7))
     few.close()
     st.close()
+
+
+@pytest.mark.parametrize("where", ["decode", "head"])
+def test_a_kernel_that_gave_up_is_noticed(lib, where):
+    """check_status() reads the workspaces of decode() and of the loss's head too: a status word as a kernel sets it
+    is raised once."""
+    import torch
+    from layer_streamed_nf4_b200.stack import Preference, Stack
+    st = Stack(CFG, tokens=16, mode="resident")
+    tgt, start = _batch(16, 640, 4)
+    pr = Preference(st, 640, tgt, start.clamp(max=16), 0.1)
+    st.decode()
+    st.check_status()
+    (st._decode_ws if where == "decode" else pr._hws)[:4].view(torch.int32).fill_(1)
+    with pytest.raises(lib.LsnError):
+        st.check_status()
+    st.check_status()
+    st.close()

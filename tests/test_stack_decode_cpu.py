@@ -56,3 +56,45 @@ def test_preference_refusals(monkeypatch, bad):
         st._distinct = False
     with pytest.raises(ValueError):
         Preference(st, **a)
+
+
+class _FakeStatus:
+    """ws_status on host memory: a non-zero first word is cleared and raised."""
+
+    def __init__(self):
+        self.read = []
+
+    def __call__(self, ws, stream=None):
+        self.read.append(ws.data_ptr())
+        word = ws[:4].view(torch.int32)
+        if int(word):
+            word.zero_()
+            raise lsnf4.LsnError(lsnf4.LSN_ERR_TIMEOUT, "fake status", "gave up")
+
+
+@pytest.mark.parametrize("where", ["decode", "head", "sweeps", "head of a second loss"])
+def test_check_status_reads_every_workspace(monkeypatch, where):
+    st, _ = _cpu_stack(monkeypatch, 2, 2, False)
+    status = _FakeStatus()
+    monkeypatch.setattr(lsnf4, "ws_status", status)
+    st.ws = [torch.zeros(256, dtype=torch.uint8)]
+    st.check_status()                                   # before any decode() or loss
+    st._decode_ws = torch.zeros(256, dtype=torch.uint8)
+    losses = []
+    for _ in range(2):
+        pr = Preference.__new__(Preference)
+        pr.stack, pr._hws = st, torch.zeros(256, dtype=torch.uint8)
+        pr._register()
+        losses.append(pr)
+    st.check_status()
+    bad = {"decode": st._decode_ws, "head": losses[0]._hws, "sweeps": st.ws[0], "head of a second loss": losses[1]._hws}[where]
+    bad[2] = 1
+    with pytest.raises(lsnf4.LsnError):
+        st.check_status()
+    st.check_status()
+    assert not st._copy()._preferences and st._copy()._decode_ws is None
+    losses.clear()                                      # a loss that is gone is not asked any more
+    del pr, bad
+    status.read.clear()
+    st.check_status()
+    assert len(status.read) == 2
