@@ -221,8 +221,11 @@ class Stack:
                 self.host[l].copy_(dblob, non_blocking=False)
         self.stream.synchronize()
 
-    def _build_tensors(self, distinct: bool):
+    def _build_tensors(self, distinct: bool, own_adapters: bool = True):
+        """Activations and gradients for T tokens; own_adapters False: A, B and the embedding table stay the ones that
+        this stack holds already (those of the stack that it is a copy of)."""
         T, r, dev = self.T, self.r, self.dev
+        keep = None if own_adapters else (self.A, self.B)
         self.x, self.dY, self.A, self.B, self.dA, self.dB = {}, {}, {}, {}, {}, {}
         # every dA [r, K] and dB [N, r] of the stack in one fp32 buffer, so that data-parallel
         # replicas sum them with one collective
@@ -234,8 +237,9 @@ class Stack:
             # token ids uniform over the vocabulary.  q, k and v take them as their input (the layer's input
             # norm is not part of the linears).
             self.token_ids = synth.device_token_ids(T, self.cfg.vocab, self.seed, device=dev)
-            self.embedding = synth.device_normal((self.cfg.vocab, self.cfg.hidden), 1.0, self.seed, synth.T_EMB,
-                                                 device=dev, dtype=torch.bfloat16)
+            if own_adapters:
+                self.embedding = synth.device_normal((self.cfg.vocab, self.cfg.hidden), 1.0, self.seed, synth.T_EMB,
+                                                     device=dev, dtype=torch.bfloat16)
             h0 = self.embedding.index_select(0, self.token_ids)
         for l in range(self.L):
             for pi, p in enumerate(self.proj):
@@ -250,13 +254,16 @@ class Stack:
                                                         dtype=torch.bfloat16) if (distinct or l == 0) else self.x[0, pi]
                 self.dY[l, pi] = synth.device_normal((T, p.N), 1.0, self.seed, la, pi, synth.T_DY, device=dev,
                                                      dtype=torch.bfloat16) if (distinct or l == 0) else self.dY[0, pi]
-                self.A[l, pi] = synth.device_uniform((r, p.K), 1.0 / p.K ** 0.5, self.seed, l, pi, synth.T_A,
-                                                     device=dev, dtype=torch.bfloat16)
-                self.B[l, pi] = synth.device_normal((p.N, r), 0.01, self.seed, l, pi, synth.T_B, device=dev,
-                                                    dtype=torch.bfloat16)
+                if own_adapters:
+                    self.A[l, pi] = synth.device_uniform((r, p.K), 1.0 / p.K ** 0.5, self.seed, l, pi, synth.T_A,
+                                                         device=dev, dtype=torch.bfloat16)
+                    self.B[l, pi] = synth.device_normal((p.N, r), 0.01, self.seed, l, pi, synth.T_B, device=dev,
+                                                        dtype=torch.bfloat16)
                 o = self.grad_offsets[l, pi]
                 self.dA[l, pi] = self.grads[o:o + r * p.K].view(r, p.K)
                 self.dB[l, pi] = self.grads[o + r * p.K:o + r * (p.K + p.N)].view(p.N, r)
+        if keep is not None:
+            self.A, self.B = keep
         nl = self.L if self.keep_outputs else 1
         self.y = {(l, pi): torch.empty((T, p.N), dtype=torch.bfloat16, device=dev)
                   for l in range(nl) for pi, p in enumerate(self.proj)}
@@ -326,13 +333,14 @@ class Stack:
         return other
 
     def with_tokens(self, tokens: int, mode: str = "streamed", n_slots: int = 2) -> "Stack":
-        """A stack sharing this one's host blobs (the frozen base) and adapters' seeds, with its own
-        activations for `tokens` tokens (a larger batch streams the same weights)."""
+        """A stack sharing this one's host blobs (the frozen base), adapters (A and B: what trains them here is seen
+        there) and embedding table, with its own activations and gradients for `tokens` tokens: a larger batch that
+        streams the same weights, or the few tokens of decode()."""
         other = self._copy()
         other.T, other.mode = tokens, mode
         other.pool, other.resident, other._calls = None, None, {}
         other.ahead = other._ahead_for(mode)
-        other._build_tensors(self._distinct)
+        other._build_tensors(self._distinct, own_adapters=False)
         other._setup_mode(n_slots)
         return other
 
@@ -454,13 +462,13 @@ class Stack:
 
     def with_inputs(self, shared_inputs: bool = True, grouped: bool = False, mode: str = "no_h2d",
                     n_slots: int = 2) -> "Stack":
-        """A stack sharing this one's host blobs, with its own activations: shared inputs per group of
-        projections, and (grouped) the groups passed to the layer calls."""
+        """A stack sharing this one's host blobs and adapters, with its own activations and gradients: shared inputs
+        per group of projections, and (grouped) the groups passed to the layer calls."""
         other = self._copy()
         other.shared_inputs, other.grouped = shared_inputs or grouped, grouped
         other.mode, other.pool, other.resident, other._calls = mode, None, None, {}
         other.ahead = other._ahead_for(mode)
-        other._build_tensors(self._distinct)
+        other._build_tensors(self._distinct, own_adapters=False)
         other._setup_mode(n_slots)
         return other
 

@@ -194,3 +194,36 @@ def test_a_kernel_that_gave_up_is_noticed(lib, where):
         st.check_status()
     st.check_status()
     st.close()
+
+
+def test_answers_come_from_the_trained_adapters(lib):
+    """A stack made by with_tokens answers with the adapters of the stack it came from, changed in place before it was
+    made or after: with B = 0 the answers are the reference's, with another B they differ from the first ones."""
+    import dataclasses
+    import torch
+    from layer_streamed_nf4_b200.stack import Stack
+    st = Stack(dataclasses.replace(CFG, vocab=320), mode="streamed", n_slots=2)
+    early = st.with_tokens(3, mode="resident")
+    early.decode()
+    torch.cuda.synchronize()
+    first = [early.y[0, i].clone() for i in range(7)]
+    for k in st.B:
+        st.B[k] *= -2
+    late = st.with_tokens(3, mode="resident")
+    for few in (early, late):
+        few.decode()
+        torch.cuda.synchronize()
+        assert any(not torch.equal(few.y[0, i], first[i]) for i in range(7))
+    assert all(torch.equal(early.y[0, i], late.y[0, i]) for i in range(7))
+    for k in st.B:
+        st.B[k].zero_()
+    for few in (early, late):
+        few.decode()
+        few.decode(adapter=False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(few.y[0, i], few.y_ref[0, i]) for i in range(7))
+    assert late.embedding is st.embedding and late.grads.data_ptr() != st.grads.data_ptr()
+    shared = st.with_inputs(mode="streamed")
+    assert all(shared.A[k] is st.A[k] and shared.B[k] is st.B[k] for k in st.A)
+    for s in (early, late, shared, st):
+        s.close()
