@@ -438,7 +438,8 @@ lsn_status preference_loss_fwd_bwd(const lsn_seq_logits* in, const double* ref_l
  * The sum is held in fp64 (squares of values too large or small for fp32
  * included); its order depends on the sizes, the alignments and on which tensors
  * lie end to end in memory (those are read as one).  A norm that
- * is infinite or NaN leaves the values unscaled and is reported as it is.
+ * is infinite or NaN, or beyond fp32's range and so reported as infinite, leaves
+ * the values unscaled.
  * t is a HOST array, read during the call only; its pointers need only their
  * type's alignment, dst may equal src (in place; nothing is written when
  * nothing is scaled) or lie apart, and the tensors may not overlap each other. */

@@ -193,8 +193,9 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_norm_kernel(const __grid_co
     if (threadIdx.x == 0) {
         const double nrm = sqrt(t);
         *norm = (float)nrm;
-        // over the largest norm: scale; a norm that is no number, or infinite, leaves the gradients as they are
-        ws->factor = nrm > (double)max_norm && nrm <= 1.7976931348623157e308 ? (float)((double)max_norm / nrm) : 1.f;
+        // over the largest norm: scale; a norm that is no number, or infinite as fp32 reports it, leaves the gradients
+        // as they are
+        ws->factor = nrm > (double)max_norm && (float)nrm < INFINITY ? (float)((double)max_norm / nrm) : 1.f;
         ws->done = 0;
     }
 }

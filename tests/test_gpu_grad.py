@@ -206,3 +206,18 @@ def test_offsets_beyond_32_bits(lib):
     src[0][-1], src[0][3] = 3.0, 4.0
     got, _ = run(lib, src, 2.5)
     assert got == 5.0 and float(src[0][-1]) == 1.5 and float(src[0][3]) == 2.0
+
+
+@pytest.mark.parametrize("std", [1e37, 3e37])
+def test_a_norm_beyond_fp32_is_infinite(lib, std):
+    """Finite gradients whose norm fp32 does not hold: reported as infinite, and nothing is scaled."""
+    import torch
+    src = make([5000, 33], ("fp32",), std=std)
+    src[0].clamp_(-3e38, 3e38)
+    assert bool(src[0].isfinite().all()) and norm64(src) > 3.5e38
+    before = [s.clone() for s in src]
+    dst = [torch.full_like(s, 5.0) for s in src]
+    got, _ = run(lib, src, 1.0, dst)
+    assert got == float("inf") and all(torch.equal(a, b) for a, b in zip(dst, before))
+    got, _ = run(lib, src, 1.0)
+    assert got == float("inf") and all(torch.equal(a, b) for a, b in zip(src, before))
