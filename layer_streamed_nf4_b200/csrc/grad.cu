@@ -28,13 +28,16 @@ struct GradArgs {
 };
 static_assert(sizeof(GradArgs<kMaxTensors>) + 64 <= 32764, "kernel parameters");
 
-// Head of the workspace: the scale for the clip kernel, the count of finished
-// CTAs (zero between calls), then one fp64 partial sum per CTA and launch.
+// Head of the workspace: the scale for the clip kernel, which multiplies by
+// both numbers in turn (pre is 1, or a power of two that keeps a scale below
+// fp32's normal range from losing bits), the count of finished CTAs (zero
+// between calls), then one fp64 partial sum per CTA and launch.
 struct GradWs {
-    float factor;
+    float pre, factor;
     int done;
     double part[1];
 };
+constexpr float kPre = 0x1p-100f;
 constexpr size_t kWsHead = 256;
 
 template <int MAX>
@@ -105,17 +108,21 @@ __device__ __forceinline__ double squares_of(const uint4& v, bool bf16) {
         return squares4(lo_bf16(v.x), hi_bf16(v.x), lo_bf16(v.y), hi_bf16(v.y)) + squares4(lo_bf16(v.z), hi_bf16(v.z), lo_bf16(v.w), hi_bf16(v.w));
     return squares4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ uint4 scaled(uint4 v, float f, bool bf16) {
+struct Scale {
+    float pre, factor;
+    __device__ __forceinline__ float operator()(float g) const { return g * pre * factor; }
+};
+__device__ __forceinline__ uint4 scaled(uint4 v, Scale f, bool bf16) {
     if (bf16) {
-        v.x = pack_bf16x2(lo_bf16(v.x) * f, hi_bf16(v.x) * f);
-        v.y = pack_bf16x2(lo_bf16(v.y) * f, hi_bf16(v.y) * f);
-        v.z = pack_bf16x2(lo_bf16(v.z) * f, hi_bf16(v.z) * f);
-        v.w = pack_bf16x2(lo_bf16(v.w) * f, hi_bf16(v.w) * f);
+        v.x = pack_bf16x2(f(lo_bf16(v.x)), f(hi_bf16(v.x)));
+        v.y = pack_bf16x2(f(lo_bf16(v.y)), f(hi_bf16(v.y)));
+        v.z = pack_bf16x2(f(lo_bf16(v.z)), f(hi_bf16(v.z)));
+        v.w = pack_bf16x2(f(lo_bf16(v.w)), f(hi_bf16(v.w)));
     } else {
-        v.x = __float_as_uint(__uint_as_float(v.x) * f);
-        v.y = __float_as_uint(__uint_as_float(v.y) * f);
-        v.z = __float_as_uint(__uint_as_float(v.z) * f);
-        v.w = __float_as_uint(__uint_as_float(v.w) * f);
+        v.x = __float_as_uint(f(__uint_as_float(v.x)));
+        v.y = __float_as_uint(f(__uint_as_float(v.y)));
+        v.z = __float_as_uint(f(__uint_as_float(v.z)));
+        v.w = __float_as_uint(f(__uint_as_float(v.w)));
     }
     return v;
 }
@@ -195,7 +202,9 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_norm_kernel(const __grid_co
         *norm = (float)nrm;
         // over the largest norm: scale; a norm that is no number, or infinite as fp32 reports it, leaves the gradients
         // as they are
-        ws->factor = nrm > (double)max_norm && (float)nrm < INFINITY ? (float)((double)max_norm / nrm) : 1.f;
+        const double f = nrm > (double)max_norm && (float)nrm < INFINITY ? (double)max_norm / nrm : 1.0;
+        ws->pre = f < kPre ? kPre : 1.f;
+        ws->factor = (float)(f < kPre ? f / kPre : f);
         ws->done = 0;
     }
 }
@@ -216,10 +225,10 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_c
     find();
     pdl_wait();
     pdl_launch_dependents();
-    const float f = ws->factor;
+    const Scale f{ws->pre, ws->factor};
     for (; ch >= 0; ch -= (int)gridDim.x, find()) {
         char* const dst = reinterpret_cast<char*>(a.dst[i]) + (c.base - reinterpret_cast<const char*>(a.src[i]));
-        if (f == 1.f && dst == c.base) continue;
+        if (f.pre == 1.f && f.factor == 1.f && dst == c.base) continue;
         const int es = c.bf16 ? 2 : 4, per = 16 / es;
         const bool wide = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
         if (wide && c.lo == 0 && c.hi == kChunkBytes / es) {            // a whole chunk: a thread's words all in flight
@@ -234,9 +243,9 @@ __global__ void __launch_bounds__(kThreads) lsn_grad_scale_kernel(const __grid_c
         for (int j = threadIdx.x; j < g.n; j += kThreads) {
             const int k = g.at(j, c, per);
             if (c.bf16)
-                reinterpret_cast<uint16_t*>(dst)[k] = __bfloat16_as_ushort(__float2bfloat16_rn(lo_bf16(reinterpret_cast<const uint16_t*>(c.base)[k]) * f));
+                reinterpret_cast<uint16_t*>(dst)[k] = __bfloat16_as_ushort(__float2bfloat16_rn(f(lo_bf16(reinterpret_cast<const uint16_t*>(c.base)[k]))));
             else
-                reinterpret_cast<float*>(dst)[k] = reinterpret_cast<const float*>(c.base)[k] * f;
+                reinterpret_cast<float*>(dst)[k] = f(reinterpret_cast<const float*>(c.base)[k]);
         }
         const uint4* const p = reinterpret_cast<const uint4*>(c.base) + g.w0 + threadIdx.x;
         uint4* const q = reinterpret_cast<uint4*>(dst) + g.w0 + threadIdx.x;

@@ -221,3 +221,29 @@ def test_a_norm_beyond_fp32_is_infinite(lib, std):
     assert got == float("inf") and all(torch.equal(a, b) for a, b in zip(dst, before))
     got, _ = run(lib, src, 1.0)
     assert got == float("inf") and all(torch.equal(a, b) for a, b in zip(src, before))
+
+
+@pytest.mark.parametrize("types", [("fp32",), ("fp32", "bf16")])
+@pytest.mark.parametrize("max_norm", [1e-3, 1e-7])
+def test_a_factor_below_the_normal_range(lib, max_norm, types):
+    """A norm of 1e38 brought down to a small one: the factor, below 2^-126, keeps its 24 bits."""
+    import torch
+    src = make([5000, 333], types, std=1e36)
+    before = [s.clone() for s in src]
+    total = norm64(src)
+    dst = [torch.empty_like(s) for s in src]
+    run(lib, src, max_norm, dst)
+    check(before, dst, total, max_norm)
+    run(lib, src, max_norm)
+    check(before, src, total, max_norm)
+
+
+def test_a_factor_next_to_the_power_of_two(lib):
+    """A factor that is 2^-100 but for a part in 2^30: scaled in place like any other."""
+    import torch
+    src = [torch.full((1,), 2.0 ** 127, device="cuda"), torch.full((4096,), 2.0 ** 100, device="cuda")]
+    total = norm64(src)
+    max_norm = float(np.nextafter(np.float32(total * 2.0 ** -100), np.float32(0)))
+    before = [s.clone() for s in src]
+    run(lib, src, max_norm)
+    check(before, src, total, max_norm)
