@@ -304,11 +304,12 @@ lsn_status lora_layer_bwd(int n, const lsn_lora_proj* p, int64_t T, int r, float
  * read straight from the packed codes: at this size the time is that of
  * reading the weights, and a bf16 copy of W would be nine times the bytes.
  * Precision: the weights enter as level (fp16, 11 significant bits) times the
- * fp32 absmax and are not rounded to bf16 as lora_linear_fwd's are, x enters
- * exactly (fp16 times a power of two per block), all sums are fp32, x A^T
- * stays fp32, and y is rounded once.  y therefore agrees with
- * lora_linear_fwd's to the rounding of its weights, not bit for bit; the
- * sum's order depends on the shapes alone.
+ * fp32 absmax and are not rounded to bf16 as lora_linear_fwd's are.  x enters
+ * as fp16 times a power of two per block of 64: exactly down to 2^-31 of the
+ * block's largest finite value, and below that to 2^-39 of that value.  All
+ * sums are fp32, x A^T stays fp32 (from x itself), and y is rounded once.  y
+ * therefore agrees with lora_linear_fwd's to the rounding of its weights, not
+ * bit for bit; the sum's order depends on the shapes alone.
  *
  * Shapes as lora_layer_fwd (K % 64 == 0, N % 64 == 0, r a multiple of 8 up to
  * 64), 0 <= T <= LSN_DECODE_MAX_T (T == 0 is a no-op); NF4 bases only

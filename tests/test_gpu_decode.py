@@ -433,3 +433,27 @@ def test_offsets_beyond_32_bits(lib, T):
         tol = tol + x[:, 64 * b:64 * b + 64].double().abs() @ W.abs().T
     tol = tol * (2.0 ** -11 + 300 * 2.0 ** -24) + want.abs() * 2.0 ** -8
     assert bool(((y.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("K", [256, 4224])
+@pytest.mark.parametrize("up", [28, 33, 38])
+def test_values_far_below_the_largest_of_their_block(lib, K, up):
+    """One value 2^up times the others in a block, against weights of zero: the others count exactly down to 2^-31 of
+    the largest, and are off by at most 2^-39 of it each below that."""
+    import torch
+    p = Proj(lib, K, 64, 3, 8, seed=4, adapter=False)
+    W = synth.normal_f32((64, K), 0.02, 1, 2)
+    W[:, 17] = 0
+    p.dw.quantize(W)
+    p.W64 = dequant64(lib, p.dw)
+    assert (p.W64[:, 17] == 0).all()
+    p.x[:, 17] = 2.0 ** up * 4
+    run_single(lib, p)
+    torch.cuda.synchronize()
+    x = p.x.double().cpu().numpy()
+    x[:, 17] = 0
+    y, s = x @ p.W64.T, np.abs(x) @ np.abs(p.W64).T
+    lost = np.where(np.abs(x[:, :64]) < 2.0 ** (up + 2 - 31), 2.0 ** (up + 2 - 39), 0.0) @ np.abs(p.W64[:, :64]).T
+    tol = np.abs(y) * 2.0 ** -8 + s * (2.0 ** -11 + (228 + K // 64) * 2.0 ** -24) + lost * (1 + 2.0 ** -7) + 1e-37
+    got = p.y[:3].double().cpu().numpy()
+    assert (np.abs(got - y) <= tol).all(), float(np.max(np.abs(got - y) / tol))
