@@ -97,6 +97,8 @@ template <> struct Words<uint16_t> {
     }
     static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
     static __device__ __forceinline__ void set(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+    // the exponential behind a gradient: off by 2^-22 and 2^-23 of its argument here, far below bf16's step
+    static __device__ __forceinline__ float exp(float x) { return ex2(x * kLog2e); }
 };
 template <> struct Words<float> {
     static constexpr int per = 4;
@@ -117,6 +119,7 @@ template <> struct Words<float> {
     }
     static __device__ __forceinline__ float one(const float* p) { return *p; }
     static __device__ __forceinline__ void set(float* p, float v) { *p = v; }
+    static __device__ __forceinline__ float exp(float x) { return expf(x); }        // 2 ulp for every argument
 };
 
 // Whether row t's target is counted: in the vocabulary, inside the sequences.
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_con
                 float v[per];
                 Words<E>::get(x[u], v);
                 #pragma unroll
-                for (int i = 0; i < per; ++i) v[i] = nc * ex2((v[i] - L) * kLog2e);
+                for (int i = 0; i < per; ++i) v[i] = nc * Words<E>::exp(v[i] - L);
                 const int at = y + p.mis - k * per;                 // the target's place in this word, in one word of the row
                 if ((unsigned)at < (unsigned)per) {
                     #pragma unroll
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_con
         const int edge = p.head + r.V - p.tail;
         if ((int)threadIdx.x < edge) {
             const int e = (int)threadIdx.x < p.head ? (int)threadIdx.x : p.tail + (int)threadIdx.x - p.head;
-            Words<E>::set(out + e, on ? nc * ex2((Words<E>::one(row + e) - L) * kLog2e) + (e == y ? c : 0.f) : 0.f);
+            Words<E>::set(out + e, on ? nc * Words<E>::exp(Words<E>::one(row + e) - L) + (e == y ? c : 0.f) : 0.f);
         }
     }
 }

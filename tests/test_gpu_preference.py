@@ -546,3 +546,20 @@ def test_one_large_logit(lib, top, dtype):
     lib.preference_loss_fwd_bwd(b.sl, None, lib.preference(0, 0.1), b.lse, b.logp, b.count, b.reward, b.loss, b.mean, b.dlogp, d, b.V, b.ws, b.nws)
     torch.cuda.synchronize()
     assert bool((b.lse[:b.T] == b.logits[0, at[0]].float()).all()) and bool((b.logp == 0).all()) and bool((d == 0).all())
+
+
+def test_fp32_probabilities_to_the_last_bits(lib):
+    """With lse = 0 and a factor of 1 the gradient is [v = y] - exp(l): expf's 2 ulp, 2^-22, however small it is."""
+    import torch
+    V, T = 1003, 7
+    logits = -torch.rand(T, V, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") * 80.0
+    tgt, st = torch.full((T,), 5, dtype=torch.int32, device="cuda"), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    sl = lib.seq_logits(logits, T, V, V, lib.LSN_DT_F32, tgt, 1, st)
+    d = torch.empty(T, V, device="cuda")
+    lib.seq_logp_bwd(sl, torch.zeros(T, device="cuda"), torch.ones(1, device="cuda"), None, d, V)
+    torch.cuda.synchronize()
+    p = logits.double().exp()
+    rel = (d.double() + p).abs() / p
+    rel[:, 5] = 0
+    assert float(rel.max()) <= 2.0 ** -22
+    assert float((d[:, 5].double() - (1 - p[:, 5])).abs().max()) <= 2.0 ** -22
