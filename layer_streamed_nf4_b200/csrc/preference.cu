@@ -250,21 +250,15 @@ struct Finish {
     Ws* ws;
 };
 
-// softplus and the logistic function: their argument comes in fp64, the part
-// that is no larger than its rounding to fp32 allows is computed in fp32.
-__device__ __forceinline__ double softplus(double v) { return fmax(v, 0.0) + (double)log1pf(expf(-fabsf((float)v))); }
-__device__ __forceinline__ float sigmoid(double v) {
-    const float e = expf(-fabsf((float)v));
-    return v >= 0 ? 1.f / (1.f + e) : e / (1.f + e);
-}
-
 // Loss and its derivative with respect to the difference h of the log ratios.
 __device__ __forceinline__ void pair_loss(const Finish& f, double h, double* loss, double* d) {
     const double b = f.beta, e = f.smooth, z = b * h;
     if (f.kind == LSN_PREF_SIGMOID) {
+        // softplus(v) = max(v, 0) + log(1 + t) and sigmoid(v) = 1 / (1 + t), or t / (1 + t) for v < 0, with t = exp(-|v|)
+        const double t = exp(-fabs(z)), rest = log1p(t), large = 1.0 / (1.0 + t), small = t * large;
         // (without smoothing the second term is left out, not multiplied by 0: it may be infinite)
-        *loss = (1.0 - e) * softplus(-z) + (e > 0.0 ? e * softplus(z) : 0.0);
-        *d = b * (e * (double)sigmoid(z) - (1.0 - e) * (double)sigmoid(-z));
+        *loss = (1.0 - e) * ((z < 0.0 ? -z : 0.0) + rest) + (e > 0.0 ? e * ((z > 0.0 ? z : 0.0) + rest) : 0.0);
+        *d = b * (z >= 0.0 ? e * large - (1.0 - e) * small : e * small - (1.0 - e) * large);
     } else if (f.kind == LSN_PREF_HINGE) {
         const bool nan = z != z;
         *loss = nan ? z : fmax(1.0 - z, 0.0);

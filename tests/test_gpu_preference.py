@@ -563,3 +563,34 @@ def test_fp32_probabilities_to_the_last_bits(lib):
     rel[:, 5] = 0
     assert float(rel.max()) <= 2.0 ** -22
     assert float((d[:, 5].double() - (1 - p[:, 5])).abs().max()) <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("e", [0.0, 0.125])
+def test_the_loss_of_exact_ratios(lib, e):
+    """No rows: every log-probability is 0 and the ratios are the reference's, exactly.  Loss and gradients are the
+    fp64 values rounded once to fp32 (2^-24), where the loss is large as where it all but vanishes."""
+    import torch
+    h = np.concatenate([np.linspace(-170, 170, 171), [0.0, 1e-9, -1e-9, 1500.0, -1500.0]])
+    P, beta = len(h), 0.5
+    ref = np.zeros(2 * P)
+    ref[1::2] = h                                                # h = (0 - 0) - (0 - ref of the rejected)
+    st = torch.zeros(2 * P + 1, dtype=torch.int32, device="cuda")
+    sl = lib.seq_logits(None, 0, 64, 64, lib.LSN_DT_F32, None, 2 * P, st)
+    f32 = lambda n: torch.full((n,), float("nan"), device="cuda")  # noqa: E731
+    loss, dlogp, mean, reward, logp = f32(P), f32(2 * P), f32(1), f32(2 * P), torch.empty(2 * P, dtype=torch.float64, device="cuda")
+    n = lib.seq_logp_ws_bytes(sl)
+    lib.preference_loss_fwd(sl, torch.from_numpy(ref).cuda(), lib.preference(0, beta, e), None, logp, None, reward, loss, mean, dlogp,
+                            torch.zeros(n, dtype=torch.uint8, device="cuda"), n)
+    torch.cuda.synchronize()
+    z = beta * h
+    t = np.exp(-np.abs(z))
+    up, down = np.maximum(-z, 0) + np.log1p(t), np.maximum(z, 0) + np.log1p(t)
+    sig = lambda v: np.where(v >= 0, 1 / (1 + t), t / (1 + t))  # noqa: E731
+    want = (1 - e) * up + e * down
+    dw = beta * (e * sig(z) - (1 - e) * sig(-z)) / P
+    half = 2.0 ** -24 * 1.001
+    assert (np.abs(loss.double().cpu().numpy() - want) <= half * want + 2.0 ** -150).all()
+    # with smoothing the two terms cancel in part: what fp64 leaves of either
+    assert (np.abs(dlogp.double().cpu().numpy()[0::2] - dw) <= half * np.abs(dw) + 2.0 ** -50 * beta / P * (e > 0) + 2.0 ** -150).all()
+    assert torch.equal(dlogp[0::2], -dlogp[1::2])
+    assert abs(float(mean) - want.mean()) <= 2.0 ** -23 * want.mean()
