@@ -134,7 +134,9 @@ __device__ __forceinline__ X16 load16(const uint16_t* p, bool on) {
 // 8 significant bits and fp16 11, and the power of two puts the largest finite
 // value into [2^14, 2^15): a value down to 2^-31 of the largest is kept exactly,
 // a smaller one to half of fp16's last step 2^-24, 2^-39 of the largest, below
-// what an fp32 sum keeps.  Infinities and NaN stay what they are.
+// what an fp32 sum keeps.  Infinities and NaN stay what they are.  A block's sum
+// takes its absmax before this scale: the other way round a block of the largest
+// inputs would leave fp32's range.
 __device__ __forceinline__ float half_x(const X16& v, uint32_t (&h)[8]) {
     uint32_t top = 0;
     #pragma unroll
@@ -658,10 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
                 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float lo = ldsf(am_sh + (16 * h + rowp) * 16 + t4 * 4), hi = ldsf(am_sh + (16 * h + 8 + rowp) * 16 + t4 * 4);
-                    acc[h][0][0] = fmaf(c[h][0] * xs2.x, lo, acc[h][0][0]);
-                    acc[h][0][1] = fmaf(c[h][1] * xs2.y, lo, acc[h][0][1]);
-                    acc[h][0][2] = fmaf(c[h][2] * xs2.x, hi, acc[h][0][2]);
-                    acc[h][0][3] = fmaf(c[h][3] * xs2.y, hi, acc[h][0][3]);
+                    acc[h][0][0] = fmaf(c[h][0] * lo, xs2.x, acc[h][0][0]);
+                    acc[h][0][1] = fmaf(c[h][1] * lo, xs2.y, acc[h][0][1]);
+                    acc[h][0][2] = fmaf(c[h][2] * hi, xs2.x, acc[h][0][2]);
+                    acc[h][0][3] = fmaf(c[h][3] * hi, xs2.y, acc[h][0][3]);
                 }
             } else {
                 // a rolled loop: unrolled, or with the next block's x read ahead, registers spill and moves
@@ -703,10 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1) lsn_decode_kernel(const __grid_co
                         for (int i = 0; i < NT; ++i) mma_f16(c[i], a, xc[i].z, xc[i].w);
                         #pragma unroll
                         for (int i = 0; i < NT; ++i) {
-                            acc[h][i][0] = fmaf(c[i][0] * xs[i].x, lo, acc[h][i][0]);
-                            acc[h][i][1] = fmaf(c[i][1] * xs[i].y, lo, acc[h][i][1]);
-                            acc[h][i][2] = fmaf(c[i][2] * xs[i].x, hi, acc[h][i][2]);
-                            acc[h][i][3] = fmaf(c[i][3] * xs[i].y, hi, acc[h][i][3]);
+                            acc[h][i][0] = fmaf(c[i][0] * lo, xs[i].x, acc[h][i][0]);
+                            acc[h][i][1] = fmaf(c[i][1] * lo, xs[i].y, acc[h][i][1]);
+                            acc[h][i][2] = fmaf(c[i][2] * hi, xs[i].x, acc[h][i][2]);
+                            acc[h][i][3] = fmaf(c[i][3] * hi, xs[i].y, acc[h][i][3]);
                         }
                     }
                 }
@@ -944,10 +946,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) lsn_decode_small_kernel(cons
                 const float lo = absmax_of(c.q[2 * h], c.s2[2 * h], offset), hi = absmax_of(c.q[2 * h + 1], c.s2[2 * h + 1], offset);
                 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    acc[h][i][0] = fmaf(d[i][0] * xs[i].x, lo, acc[h][i][0]);
-                    acc[h][i][1] = fmaf(d[i][1] * xs[i].y, lo, acc[h][i][1]);
-                    acc[h][i][2] = fmaf(d[i][2] * xs[i].x, hi, acc[h][i][2]);
-                    acc[h][i][3] = fmaf(d[i][3] * xs[i].y, hi, acc[h][i][3]);
+                    acc[h][i][0] = fmaf(d[i][0] * lo, xs[i].x, acc[h][i][0]);
+                    acc[h][i][1] = fmaf(d[i][1] * lo, xs[i].y, acc[h][i][1]);
+                    acc[h][i][2] = fmaf(d[i][2] * hi, xs[i].x, acc[h][i][2]);
+                    acc[h][i][3] = fmaf(d[i][3] * hi, xs[i].y, acc[h][i][3]);
                 }
             }
         }

@@ -457,3 +457,15 @@ def test_values_far_below_the_largest_of_their_block(lib, K, up):
     tol = np.abs(y) * 2.0 ** -8 + s * (2.0 ** -11 + (228 + K // 64) * 2.0 ** -24) + lost * (1 + 2.0 ** -7) + 1e-37
     got = p.y[:3].double().cpu().numpy()
     assert (np.abs(got - y) <= tol).all(), float(np.max(np.abs(got - y) / tol))
+
+
+@pytest.mark.parametrize("K", [256, 4224])
+@pytest.mark.parametrize("T", [1, 2, 5, 11])
+def test_a_block_of_the_largest_inputs(lib, T, K):
+    """A block of values of 1e38: its sum with the levels alone leaves fp32's range, with the absmax it does not."""
+    import torch
+    p = Proj(lib, K, 64, T, 8, seed=40, adapter=False)
+    p.x[:, 64:128] = torch.where(p.x[:, 64:128] > 0, 1e38, -1e38)
+    run_single(lib, p)
+    torch.cuda.synchronize()
+    p.check()
