@@ -64,6 +64,26 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e);      // 1.9e-8: what fp32's log2 e leaves out
+
+// 2^t for t <= 1/2, within about an ulp either way: ex2.approx is 5.0e-8 low on
+// average, which adds up where a sum is scaled several times.  The series of
+// exp(f ln 2) for |f| <= 1/2 to the 7th power (the 8th is below 5.3e-9).
+__device__ __forceinline__ float exp2_even(float t) {
+    t = fmaxf(t, -127.f);                   // and what is below 2^-126 counts as 0
+    const float n = rintf(t), f = (t - n) * 0.6931471805599453f;
+    float p = 1.f / 5040.f;
+    p = fmaf(p, f, 1.f / 720.f);
+    p = fmaf(p, f, 1.f / 120.f);
+    p = fmaf(p, f, 1.f / 24.f);
+    p = fmaf(p, f, 1.f / 6.f);
+    p = fmaf(p, f, 0.5f);
+    p = fmaf(p, f, 1.f);
+    p = fmaf(p, f, 1.f);
+    return n < -126.f ? 0.f : p * __int_as_float(((int)n + 127) << 23);
+}
+// exp(x) for a difference x <= 0 of two numbers
+__device__ __forceinline__ float exp_even(float x) { return exp2_even(fmaf(x, kLog2e, x * kLog2eRest)); }
 // Maxima below it take one multiply-add a logit: the rounding of their product with
 // log2 e, which is left in the sum until the end, is at most 2^-8 there.  (From 2^31
 // on it leaves exp2's range.)
@@ -127,14 +147,9 @@ __device__ __forceinline__ bool scored(const Rows& r, int t, int y) {
     return y >= 0 && y < r.V && t >= r.start[0] && t < r.start[r.n_seq];
 }
 
-// A maximum m and the sum s of exp(x - m), joined with another such pair.
-// m = -infinity stands for "no finite value yet" and subtracts nothing.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-    const float top = fmaxf(m, m2);
-    const float at = top == -INFINITY ? 0.f : top;
-    s = s * ex2((m - at) * kLog2e) + s2 * ex2((m2 - at) * kLog2e);
-    m = top;
-}
+// The sum s of exp(x - m) about another maximum `at` >= m.  m = -infinity stands
+// for "no finite value yet"; NaN stays NaN.
+__device__ __forceinline__ float about(float m, float s, float at) { return s * exp_even(m - (at == -INFINITY ? 0.f : at)); }
 
 // The 16-byte words of a row that can be taken whole, counted from `row`
 // rounded down to 16 bytes (word w holds elements w per - mis ..): all full
@@ -159,6 +174,9 @@ __device__ __forceinline__ Piece piece_of(const void* row, int V, int split, int
 
 // (m, s) of one piece of one row per CTA, and the target's logit.  Each thread
 // keeps four 16-byte loads in flight; maxima of bf16 are taken two at a time.
+// A thread's sum is scaled once to the CTA's maximum, and evenly (exp2_even): at
+// every join by ex2.approx it came out 1.0 to 1.3e-7 low, token after token,
+// now 1.5e-8 (1000 tokens of a 152k vocabulary: their sum off by 1e-5).
 // Bound by DRAM and, nearly as much, the special-function unit (one exp2 a
 // logit): 2048 x 151936 bf16, three quarters scored, 77 us, 6.1 TB/s.  With
 // exp2((x - m) log2 e) in two instructions it took 94 us, with the words behind
@@ -190,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
         if (fabsf(top) < kSmallMax) {
             // c is a number like any other: what its rounding leaves out is put right at the end
             const float c1 = top * kLog2e;
-            if (c1 != c) s *= ex2(fabsf(old) < kSmallMax ? c - c1 : fmaf(old, kLog2e, -c1));
+            if (c1 != c) s *= exp2_even(fabsf(old) < kSmallMax ? c - c1 : fmaf(old, kLog2e, -c1));
             c = c1;
             #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -202,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
             }
         } else {                                        // masks of any size, infinities, nothing yet
             const float at = top == -INFINITY ? 0.f : top;
-            if (top != old) s *= ex2(fabsf(old) < kSmallMax ? -fmaf(at, kLog2e, -c) : (old - at) * kLog2e);
+            if (top != old) s *= fabsf(old) < kSmallMax ? exp2_even(-fmaf(at, kLog2e, -c)) : exp_even(old - at);
             #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float v[per];
@@ -212,23 +230,35 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_stats_kernel(const __grid_co
             }
         }
     }
-    if (fabsf(m) < kSmallMax) s *= ex2(-fmaf(m, kLog2e, -c));
+    if (fabsf(m) < kSmallMax) s *= exp2_even(-fmaf(m, kLog2e, -c));
     if (split == 0) {
         if (threadIdx.x == 0) ly[t] = Words<E>::one(row + y);
         const int edge = p.head + r.V - p.tail;
         if ((int)threadIdx.x < edge) {
             const int e = (int)threadIdx.x < p.head ? (int)threadIdx.x : p.tail + (int)threadIdx.x - p.head;
             const float x = Words<E>::one(row + e);
-            join(m, s, x, x == -INFINITY ? 0.f : x - x + 1.f);     // NaN and +infinity give NaN
+            const float top = fmaxf(m, x);
+            s = about(m, s, top) + about(x, x == -INFINITY ? 0.f : x - x + 1.f, top);     // NaN and +infinity give NaN
+            m = top;
         }
     }
+    float top = m;
     #pragma unroll
-    for (int o = 16; o; o >>= 1) join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(m, s);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    s = about(m, s, top);
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(top, s);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) join(m, s, sh[w].x, sh[w].y);
-        part[blockIdx.x] = make_float2(m, s);
+    if (threadIdx.x < 32) {                             // the warps', by the lanes of the first
+        const float2 w = threadIdx.x < kThreads / 32 ? sh[threadIdx.x] : make_float2(-INFINITY, 0.f);
+        top = w.x;
+        #pragma unroll
+        for (int o = kThreads / 64; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        s = about(w.x, w.y, top);
+        #pragma unroll
+        for (int o = kThreads / 64; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) part[blockIdx.x] = make_float2(top, s);
     }
 }
 
@@ -291,21 +321,47 @@ __global__ void __launch_bounds__(kFinThreads) lsn_seq_finish_kernel(const __gri
     const bool have = q < r.n_seq;
     const int a = have ? max(r.start[q], 0) : 0, b = have ? min(r.start[q + 1], r.T) : 0;
     const double ref0 = f.ref ? f.ref[2 * blockIdx.x] : 0.0, ref1 = f.ref ? f.ref[2 * blockIdx.x + 1] : 0.0;     // (pairs only)
+    // eight lanes to a row that has many pieces (37 x 151936 scored, 32 pieces: 9.7 us, with one lane 13.3; 2 to 4
+    // pieces are one round of loads for one lane)
+    const int lg = r.splits > 4 ? 3 : 0, lane0 = tid & ((1 << lg) - 1), t1 = a + (tid >> lg);
     const bool on0 = a + tid < b && scored(r, a + tid, r.targets[a + tid]);
+    const bool on1 = lg == 0 ? on0 : t1 < b && scored(r, t1, r.targets[t1]);
     if (r.T > 0) pdl_wait();
     pdl_launch_dependents();
     double sum = 0.0;
     int n = 0;
-    for (int t = a + tid; t < b; t += kHalf) {
-        float l = 0.f;
-        if (t == a + tid ? on0 : scored(r, t, r.targets[t])) {
-            float m = -INFINITY, s = 0.f;
-            #pragma unroll 4
-            for (int i = 0; i < r.splits; ++i) {
-                const float2 p = f.part[(int64_t)t * r.splits + i];
-                join(m, s, p.x, p.y);
+    for (int t0 = a; t0 < b; t0 += kHalf >> lg) {       // the same rounds for a whole warp
+        const int t = t0 + (tid >> lg);
+        const bool on = t0 == a ? on1 : t < b && scored(r, t, r.targets[t]);
+        const float2* const part = f.part + (int64_t)t * r.splits;
+        const int end = on ? r.splits : 0;
+        float m = -INFINITY;
+        double s = 0.0;
+        for (int i0 = lane0; i0 < end; i0 += 4 << lg) { // four pieces in flight
+            float2 p[4];
+            float top = m;
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + (k << lg);
+                p[k] = i < end ? part[i] : make_float2(-INFINITY, 0.f);
+                top = fmaxf(top, p[k].x);
             }
-            const double ls = log((double)s);
+            s *= (double)about(m, 1.f, top);
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) s += (double)about(p[k].x, p[k].y, top);
+            m = top;
+        }
+        if (lg > 0) {
+            float top = m;
+            for (int o = (1 << lg) >> 1; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            s *= (double)about(m, 1.f, top);
+            m = top;
+            for (int o = (1 << lg) >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        }
+        if (t >= b || lane0 != 0) continue;
+        float l = 0.f;
+        if (on) {
+            const double ls = log(s);
             l = (float)((double)m + ls);
             sum += ((double)f.ly[t] - (double)m) - ls;
             ++n;

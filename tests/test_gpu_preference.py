@@ -594,3 +594,19 @@ def test_the_loss_of_exact_ratios(lib, e):
     assert (np.abs(dlogp.double().cpu().numpy()[0::2] - dw) <= half * np.abs(dw) + 2.0 ** -50 * beta / P * (e > 0) + 2.0 ** -150).all()
     assert torch.equal(dlogp[0::2], -dlogp[1::2])
     assert abs(float(mean) - want.mean()) <= 2.0 ** -23 * want.mean()
+
+
+@pytest.mark.parametrize("dtype,T,V", [("bf16", 300, 151936), ("fp32", 300, 151936), ("fp32", 500, 60000), ("bf16", 1200, 9000)])
+def test_errors_do_not_add_up_over_tokens(lib, dtype, T, V):
+    """The error of a long sequence's log-probability, by token: each exponential is 5.2e-8 low on average at most
+    (ex2.approx's mean over its arguments) and 1.3e-8 high for each unit below its thread's maximum (fp32's log2 e);
+    what scales and joins the sums errs evenly, and all that is random averages out over hundreds of tokens."""
+    import torch
+    b = Batch(lib, (T - 40, 40), V, dtype=dtype, seed=12, prompt=0.0)
+    lib.seq_logp_fwd(b.sl, b.lse, b.logp, b.count, b.ws, b.nws)
+    torch.cuda.synchronize()
+    want = 0.0
+    for t in range(0, T - 40, 100):
+        x = b.logits[t:min(t + 100, T - 40), :V].double()
+        want += float((x.gather(1, b.tgt[t:t + len(x), None].long())[:, 0] - torch.logsumexp(x, 1)).sum())
+    assert abs(float(b.logp[0]) - want) <= (T - 40) * 2.0 ** -24
