@@ -41,7 +41,9 @@
  *    unit reads rows in 16-byte units), but for the calls that state their own
  *    alignments (the preference loss, the gradient norm).
  *  - Results are deterministic: the same inputs and shapes give the same bits,
- *    independent of pointers, streams or what ran before.
+ *    independent of pointers, streams or what ran before (the log-probabilities
+ *    and the gradient norm add up in an order that also depends on how their
+ *    tensors lie against 16 bytes).
  */
 #ifndef LSNF4_H
 #define LSNF4_H
@@ -322,7 +324,8 @@ lsn_status lora_layer_bwd(int n, const lsn_lora_proj* p, int64_t T, int r, float
 /* Workspace bytes of lora_linear_decode (n = 1) and lora_layer_decode for these
  * projections, T tokens and this rank (0 when an argument is invalid).  It
  * starts with the kernels' status word (lsn_ws_status): zero-fill a new
- * workspace once. */
+ * workspace once.  Calls that may run at the same time (other streams, captured
+ * graphs replayed side by side) need one each. */
 size_t lsn_decode_ws_bytes(int n, const lsn_lora_proj* p, int64_t T, int r);
 
 lsn_status lora_linear_decode(const lsn_base* W, const uint16_t* x, int64_t T, const uint16_t* A, const uint16_t* B,
@@ -381,7 +384,13 @@ lsn_status lsn_selftest_wait_timeout(int limit_us, lsn_stream_t stream);
  * V.. of a padded row are not touched.  seq_start may change between replays
  * of a captured call.  Infinite logits: -infinity is a token that cannot
  * occur; a row holding +infinity or NaN, or nothing but -infinity, makes its
- * pair's loss and gradients NaN and no other's. */
+ * pair's loss and gradients NaN and no other's.  Finite masks of any size (-1e4,
+ * -1e30, the type's lowest value) take no probability beside larger logits.
+ * lse is rounded to fp32, and the gradients' probabilities are exp(l - lse):
+ * good to |lse| 2^-24, which is nothing for logits of ordinary size but all of
+ * it where a row's LARGEST logit is 1e7 or more in magnitude (logp, from the
+ * unrounded value, stays right there).  The order of a row's sums depends on
+ * T, V and how the row lies against 16 bytes. */
 typedef enum { LSN_DT_BF16 = 0, LSN_DT_F32 = 1 } lsn_dtype;
 typedef enum { LSN_PREF_SIGMOID = 0, LSN_PREF_HINGE = 1, LSN_PREF_SQUARED = 2 } lsn_preference_kind;
 
@@ -451,7 +460,8 @@ typedef struct {
     int dtype;                 /* lsn_dtype */
 } lsn_grad;
 
-/* Workspace bytes for n tensors.  Zero-fill it once when it is allocated. */
+/* Workspace bytes for n tensors.  Zero-fill it once when it is allocated; calls
+ * that may run at the same time need one each. */
 size_t lsn_grad_ws_bytes(int n);
 
 /* norm [1] fp32 (device). */
@@ -527,11 +537,13 @@ lsn_status lsn_timing_read(lsn_kernel_timing* out);
  *                      (barriers, tensor memory, tensor-map prefetch) overlaps
  *                      the tail of the kernel before it on the same stream;
  *                      every kernel still waits for its predecessor to finish
- *                      before it reads or writes global memory (the few-token
- *                      linears' main kernel reads its weights while the
- *                      preparation kernel of the same call runs, which itself
- *                      began after everything before the call).  0: ordinary
- *                      stream-ordered launches.
+ *                      before it reads or writes global memory (in a call of
+ *                      several kernels the later ones may read what the call
+ *                      does not write, the few-token linears' weights and the
+ *                      preference loss's targets, sequences, reference values
+ *                      and logits, while the earlier ones run, which
+ *                      themselves began after everything before the call).
+ *                      0: ordinary stream-ordered launches.
  *   LSN_OPT_GEMM_MIN_UNITS 1: a GEMM whose tiles take R rounds over all the
  *                      SMs runs on the fewest SMs that still finish in R
  *                      rounds (e.g. 128 tiles of 256 x 256: 64 SM pairs

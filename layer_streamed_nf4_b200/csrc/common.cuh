@@ -155,7 +155,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 // as this grid's CTAs leave and run their own set-up); pdl_wait blocks until
 // the grid this one depends on has finished and its memory writes are
 // visible.  Every kernel launched with the attribute calls pdl_wait before
-// its first global-memory access.  Both are no-ops for an ordinary launch.
+// its first global-memory access, but for the later kernels of a call of
+// several (few-token linears, preference loss): what the kernel ahead of them
+// does not write they may read before it, since that one waited before it let
+// them start, and all that is older was complete then.  Prefetches into the L2
+// read nothing and need not wait.  Both are no-ops for an ordinary launch.
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

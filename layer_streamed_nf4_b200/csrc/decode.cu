@@ -11,7 +11,11 @@
 // and those issue at half the rate of others).  The pair is an A register of
 // mma.sync m16n8k16: with at most 16 columns the warp-level instruction, 0.475
 // a clock and SM, costs a sixth of the lookups' time, and a tcgen05 tile would
-// stand nearly empty.  The levels in fp16 carry 11 significant bits (2^-11).
+// stand nearly empty.  The levels are rounded to fp16, 1.8e-4 of a weight on
+// average, which is little beside the rounding of y to bf16 (y's error against 64
+// bits is 1.667e-3, with exact levels 1.657e-3).  A second fp16 for what the first
+// leaves out, in 8-byte entries and with twice the MMAs, took 54 us where this
+// takes 40 (8B layer, one token), and 63 against 49 (8 tokens).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -495,7 +499,7 @@ __device__ __forceinline__ void add_adapter(const DecodeArgs& a, const DecodePro
 //
 // Bound by instruction issue and the table's loads, with about 10 us of launch,
 // preparation and joins: 8B layer in a CUDA graph (floor 17.8 us), one token
-// 40.0 us, 8 tokens 49.2, 16 tokens 66.5; 72B down, 8 tokens 57 to 64 us by
+// 39.8 us, 8 tokens 48.9, 16 tokens 66.6; 72B down, 8 tokens 57 to 64 us by
 // machine (floor 19.6).  Stages shared by the CTA, filled and scaled by producer warps, took
 // 48-55 us where this took 46 (the absmax values of 512 rows kept them behind).
 //

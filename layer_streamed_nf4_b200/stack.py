@@ -666,7 +666,8 @@ class Stack:
 
     def clip_grads(self, max_norm: float) -> torch.Tensor:
         """Scale every dA and dB down so that their global norm is at most max_norm; the norm before that, [1] on the
-        device.  (Data-parallel replicas clip after they have summed their gradients.)"""
+        device.  (Data-parallel replicas clip after they have summed their gradients, accumulated steps after the last
+        one.)  The descriptors of all tensors are made at the first call and kept."""
         if getattr(self, "_clip", None) is None or self._clip[0] is not self.grads:
             arr = lsnf4.grad_array([lsnf4.grad_tensor(g, g.numel(), lsnf4.LSN_DT_F32)
                                     for k in self.grad_offsets for g in (self.dA[k], self.dB[k])])
@@ -685,7 +686,8 @@ class Stack:
         both forwards, so the step copies as many layers as a plain one); recompute: every layer's forward
         runs again inside the backward sweep, as with activation checkpointing; preference: the loss whose
         gradient enters the backward sweep (implies reference); max_norm: the largest global norm of the adapter
-        gradients (clip_grads)."""
+        gradients (clip_grads).  Of steps that accumulate, pass it to the last one alone: it clips what the buffers
+        hold, the sum so far."""
         self.forward(reference=reference or preference is not None)
         if preference is not None:
             preference.run()
