@@ -386,11 +386,10 @@ lsn_status lsn_selftest_wait_timeout(int limit_us, lsn_stream_t stream);
  * occur; a row holding +infinity or NaN, or nothing but -infinity, makes its
  * pair's loss and gradients NaN and no other's.  Finite masks of any size (-1e4,
  * -1e30, the type's lowest value) take no probability beside larger logits.
- * lse is rounded to fp32, and the gradients' probabilities are exp(l - lse):
- * good to |lse| 2^-24, which is nothing for logits of ordinary size but all of
- * it where a row's LARGEST logit is 1e7 or more in magnitude (logp, from the
- * unrounded value, stays right there).  The order of a row's sums depends on
- * T, V and how the row lies against 16 bytes. */
+ * lse is rounded to fp32, and the gradients' probabilities are exp(l - lse),
+ * good to |lse| 2^-24, up to |lse| = 4096; rows beyond that (all of whose
+ * logits are a mask, say) take them from the logits once more.  The order of a
+ * row's sums depends on T, V and how the row lies against 16 bytes. */
 typedef enum { LSN_DT_BF16 = 0, LSN_DT_F32 = 1 } lsn_dtype;
 typedef enum { LSN_PREF_SIGMOID = 0, LSN_PREF_HINGE = 1, LSN_PREF_SQUARED = 2 } lsn_preference_kind;
 

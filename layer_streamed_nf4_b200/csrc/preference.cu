@@ -479,6 +479,34 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A row whose lse is so far from zero that fp32 holds too little of it (rows of
+// which a mask leaves nothing, say): its maximum and sum once more from the
+// logits, dl = c ([v = y] - exp(l - m) / s), by one CTA, so that it may be in
+// place.  Not inlined: it is rare, and its registers would be the common path's.
+constexpr float kFarLse = 4096.f;          // 2^-13 of a probability
+template <class E>
+__device__ __noinline__ void far_row(const E* row, E* out, int V, int y, float c) {
+    __shared__ float sh[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float m = -INFINITY, s = 0.f;
+    for (int v = threadIdx.x; v < V; v += kThreads) m = fmaxf(m, Words<E>::one(row + v));
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) sh[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, sh[w]);
+    for (int v = threadIdx.x; v < V; v += kThreads) s += expf(Words<E>::one(row + v) - m);
+    #pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __syncthreads();
+    if (lane == 0) sh[warp] = s;
+    __syncthreads();                        // every thread has read the row
+    s = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) s += sh[w];
+    const float f = -c / s;
+    for (int v = threadIdx.x; v < V; v += kThreads) Words<E>::set(out + v, fmaf(f, expf(Words<E>::one(row + v) - m), v == y ? c : 0.f));
+}
+
 // dl = c ([v = y] - exp(l - lse)), zero in rows that are not scored.  One piece
 // of a row per CTA, the last rows first: they are what the statistics kernel
 // read last and the L2 still holds (2048 x 151936 bf16: 4 us of 269 for the
@@ -520,6 +548,10 @@ __global__ void __launch_bounds__(kThreads) lsn_seq_grad_kernel(const __grid_con
         }
     }
     const float nc = -c, L = on ? lse[t] : 0.f;
+    if (fabsf(L) >= kFarLse && fabsf(L) < INFINITY) {
+        if (split == 0) far_row<E>(row, out, r.V, y, c);
+        return;
+    }
     if (!on) {
         for (int w = p.w0 + threadIdx.x; w < p.w1; w += kThreads) __stcs(&outs[w], make_uint4(0, 0, 0, 0));
     } else {

@@ -610,3 +610,44 @@ def test_errors_do_not_add_up_over_tokens(lib, dtype, T, V):
         x = b.logits[t:min(t + 100, T - 40), :V].double()
         want += float((x.gather(1, b.tgt[t:t + len(x), None].long())[:, 0] - torch.logsumexp(x, 1)).sum())
     assert abs(float(b.logp[0]) - want) <= (T - 40) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V,pad,offset", [(700, 0, 0), (32003, 5, 3)])
+@pytest.mark.parametrize("level", [5000.0, -7e4, -1e9, -1e30, "lowest", 1e10])
+def test_gradients_of_rows_far_from_zero(lib, level, V, pad, offset, dtype):
+    """Rows of which a mask leaves nothing (all one number), of two numbers, and ordinary ones lifted by 5000: their
+    probabilities do not depend on the level.  Apart, in one call and in place: the same bits."""
+    import torch
+    b = Batch(lib, (6, 8), V, pad, dtype, 2, seed=5, prompt=0.2, offset=offset)
+    top = torch.finfo(b.dt).min if level == "lowest" else level
+    for t in range(0, b.T - 2, 3):
+        b.logits[t, :V] = top
+        if t % 2 and level != "lowest":
+            b.logits[t, :V // 3] = top * (1 if top < 0 else -1) * 2
+    if level == 5000.0:
+        b.logits[1:b.T - 2:3, :V] += level
+    x = b.logits[:, :V].double()
+    p = lib.preference(lib.LSN_PREF_SIGMOID, 0.1)
+    d1, d2 = (torch.full((b.T, V + 3), 9.0, dtype=b.dt, device="cuda") for _ in range(2))
+    a = b.refd, p, b.lse, b.logp, b.count, b.reward, b.loss, b.mean, b.dlogp
+    lib.preference_loss_fwd_bwd(b.sl, *a, d1, V + 3, b.ws, b.nws)
+    lib.seq_logp_bwd(b.sl, b.lse, b.dlogp, b.count, d2, V + 3)
+    lib.preference_loss_fwd_bwd(b.sl, *a, b.logits, b.ld, b.ws, b.nws)
+    torch.cuda.synchronize()
+    assert torch.equal(d1, d2) and torch.equal(d1[:, :V], b.logits[:, :V]) and bool((d1[:, V:] == 9).all())
+    m = x.amax(1, keepdim=True)
+    prob = (x - m).exp()
+    prob /= prob.sum(1, keepdim=True)
+    on = torch.from_numpy((b.targets >= 0) & (b.targets < V) & (np.arange(b.T) < b.start[-1])).cuda()
+    hot = torch.zeros_like(x).scatter_(1, b.tgt.long().clamp(0, V - 1)[:, None], 1.0)
+    seq = np.clip(np.searchsorted(b.start, np.arange(b.T), side="right") - 1, 0, b.n - 1)
+    c = (b.dlogp.double()[torch.from_numpy(seq).cuda()] * on)[:, None]
+    want = c * (hot - prob)
+    # the lse of a row below 4096 is off by 2^-13 at most; the argument's roundings, ex2, sums and the output's step
+    near = (m[:, 0].abs() < 4096)[:, None] * (m.abs() + 20.0) * 2.0 ** -24
+    rel = near + b.tol_s(np.zeros(1)) + 2.0 ** -22 + 2 * (x - m).abs().clamp_max(200) * 1.45 * 2.0 ** -24
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    tol = c.abs() * prob * rel + c.abs() * (hot + prob) * 2.0 ** -23 + want.abs() * half + 1e-37
+    bad = ~((d1[:, :V].double() - want).abs() <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), torch.nonzero(bad)[:3])
